@@ -36,10 +36,14 @@ typedef enum {
     RCX_ERR_UNSUPPORTED = -2,    /* valid request this build has no path for  */
     RCX_ERR_ALIGNMENT = -3,      /* pointer or stride breaks a vector/TMA rule */
     RCX_ERR_CUDA = -4,           /* a CUDA runtime/driver call failed          */
-    RCX_ERR_DEVICE_TIMEOUT = -5  /* a device-side bounded wait gave up         */
+    RCX_ERR_DEVICE_TIMEOUT = -5, /* a device-side bounded wait gave up         */
+    RCX_ERR_DEVICE_INDEX = -6    /* a length or block number on the device was
+                                    out of range (rcx_kv_blocks calls)         */
 } rcx_status;
 
-typedef enum { RCX_F32 = 0, RCX_BF16 = 1, RCX_I8 = 2 /* int8 KV-cache codes only */ } rcx_dtype;
+/* RCX_I8 and RCX_E4M3 (8-bit floats, 4 exponent and 3 fraction bits): KV-cache
+ * codes only. */
+typedef enum { RCX_F32 = 0, RCX_BF16 = 1, RCX_I8 = 2, RCX_E4M3 = 3 } rcx_dtype;
 
 /* RoPE frequency schedules (see rcx_rope_freqs). */
 typedef enum {
@@ -124,6 +128,41 @@ int rcx_rope_freqs_per_pair(double base, int d, const double* factors, double* i
 int rcx_rope_apply(rcx_tensor q, rcx_tensor k, rcx_tensor q_out, rcx_tensor k_out,
                    const int64_t* positions, int64_t n_positions,
                    const double* inv_freq, void* stream);
+
+/*
+ * rcx_rope_axes_map -- the axis of each of a head's `pairs` pairs when axis a
+ * owns sections[a] pairs (their sum is `pairs`): one section after another, or
+ * (interleaved != 0) dealt out in turn, one pair of each axis that has some
+ * left.  Host arrays; n_axes 1..256, sections >= 0.  Returns
+ * RCX_ERR_INVALID_ARG on a bad argument (output untouched).
+ */
+int rcx_rope_axes_map(const int64_t* sections, int n_axes, int interleaved, int pairs, int32_t* axis_out);
+
+/* rcx_rope_axes_apply flags */
+enum {
+    RCX_ROPE_HALVES = 1,   /* pairs (i, i + d/2) instead of (2i, 2i + 1)   */
+    RCX_ROPE_INVERSE = 2   /* turn back: R(m)^T, the rotation's gradient   */
+};
+
+/*
+ * rcx_rope_axes_apply -- rotate Q and/or K by positions on several axes (time,
+ * height and width of an image or video token; "Context Extension" concept
+ * page, Technical principles, with one position per axis): pair i of token n of
+ * sequence b turns by phi_i = positions[axis[i]][b][n] * inv_freq[i].  The
+ * rotation is orthogonal, so with RCX_ROPE_INVERSE the same call is its
+ * gradient: (dq, dk) from the gradients of the outputs.
+ *
+ * q, k, q_out, k_out: as rcx_rope_apply (in place where out.ptr == in.ptr with
+ * the same strides; an operand whose in.ptr is NULL is skipped), with d a
+ * multiple of 16 (bf16) or 8 (f32), at most 256, and one dtype for all four.
+ * positions: device int64; entry (axis, b, n) at axis * stride_axis + b *
+ * stride_batch + n (a stride of 0 shares a row); n_axes 1..256.  inv_freq: HOST
+ * d/2 doubles (a pair with 0 stays as it is).  axis: HOST d/2 entries in [0,
+ * n_axes).  Angles as in rcx_rope_apply.  Memory-bound.
+ */
+int rcx_rope_axes_apply(rcx_tensor q, rcx_tensor k, rcx_tensor q_out, rcx_tensor k_out,
+                        const int64_t* positions, int n_axes, int64_t stride_axis, int64_t stride_batch,
+                        const double* inv_freq, const int32_t* axis, int flags, void* stream);
 
 /*
  * rcx_attn_blockwise_fwd -- causal attention forward with an online softmax
@@ -260,6 +299,94 @@ int rcx_attn_decode_int8_fwd(rcx_tensor q, rcx_tensor k, const float* k_scale, r
                              int rope_flags, void* workspace, int64_t workspace_bytes, void* stream);
 
 /*
+ * Block-scaled paged KV cache ("Context window extension: 4K to 1M" 6.1, the KV
+ * cache in 8 bits instead of 16; the "Context Extension" concept page lists the
+ * same compression).  Tokens live in blocks of `block` tokens; a block belongs
+ * to one sequence, and per KV head it has one fp32 scale for K and one for V: a
+ * stored value is code * scale.  Block j of sequence b is pool entry
+ * table[b * table_stride + j].
+ *
+ * k, v: pools of codes [n_blocks, block, Hkv, d], RCX_I8 or RCX_E4M3 (one type
+ * for both); block 16, 32, 64 or 128; d 64 or 128; stride[3] == 1, base pointers
+ * and the other strides multiples of 16 bytes (the layout may be
+ * [n_blocks, Hkv, block, d] underneath).  k_scale, v_scale: device fp32
+ * [n_blocks, Hkv], contiguous.  table: device int32 [B, width]; entries of
+ * blocks that hold no token of the sequence are not read.
+ *
+ * Scale and code of a block whose largest |x| is amax (0: scale 0, codes 0):
+ *   RCX_I8:   s = fl(amax / 127), at least 2^-120; code = rint(x * fl(1 / s)),
+ *             the product unrounded, ties to even
+ *   RCX_E4M3: s = the smallest power of two with amax <= 448 s (2^-120 ..
+ *             2^120); code = e4m3(x / s), ties to even
+ * A block given an infinity or NaN gets scale NaN: its tokens read back as NaN.
+ * The NaN codes of RCX_E4M3 are never written; readers take them as +-480.
+ *
+ * Lengths and block numbers are device data, so their errors show on the device:
+ * a sequence whose start, count or length is negative or over the table's
+ * capacity (or count over N) counts as having no tokens, a block number outside
+ * [0, n_blocks) is not followed (append writes nothing there, read gives zeros,
+ * attention uses block 0 instead), and rcx_device_status() reports
+ * RCX_ERR_DEVICE_INDEX.  Calls that only read may share blocks between
+ * sequences; a block that append writes must belong to one sequence.
+ */
+typedef struct {
+    rcx_tensor k, v;
+    float* k_scale;
+    float* v_scale;
+    const int32_t* table;
+    int64_t B, width, table_stride;
+} rcx_kv_blocks;
+
+/*
+ * rcx_kv_block_append -- write tokens start[b] .. start[b] + count[b] - 1 of each
+ * sequence into its blocks.  A block that already holds tokens keeps the larger
+ * of its scale and the new tokens'; where it grows, the codes already there
+ * become rint(code * fl(s_old / s_new)) (e4m3(code * s_old / s_new)).  Codes
+ * behind the new tokens, and blocks that get none, stay as they are.
+ *
+ * k, v: new tokens [B, N, Hkv, d], bf16 or f32 (one dtype), 16-byte aligned base
+ * and strides; row i of sequence b is its token start[b] + i.  start, count:
+ * device int64 [B]; count NULL means N each.  Reads each value and writes each
+ * code once.  Launches are timed under RCX_KERNEL_DECODE.
+ */
+int rcx_kv_block_append(rcx_tensor k, rcx_tensor v, const rcx_kv_blocks* cache, const int64_t* start,
+                        const int64_t* count, void* stream);
+
+/*
+ * rcx_kv_block_read -- the first n tokens of each sequence as k_out, v_out
+ * [B, n, Hkv, d] (bf16 or f32, one dtype, 16-byte aligned base and strides):
+ * fl(code * scale) rounded to the dtype, and zeros from token len[b] on.  len:
+ * device int64 [B].
+ */
+int rcx_kv_block_read(const rcx_kv_blocks* cache, const int64_t* len, rcx_tensor k_out, rcx_tensor v_out,
+                      void* stream);
+
+/*
+ * rcx_attn_kv_block_fwd -- attention of the last tokens of each sequence over
+ * the cache that holds them: query row i < count[b] of sequence b is its token
+ * start[b] + i and sees tokens j <= start[b] + i of the cache (append them
+ * first), with the window, sinks, GQA, temperature and LSE of
+ * rcx_attn_blockwise_fwd.  N = 1 is a decoding step, a few rows a check of
+ * drafted tokens, many a chunk of a prompt.  Rows from count[b] on get O = 0,
+ * lse = -inf.
+ *
+ * q: [B, N, Hq, d] bf16, already rotated, 16-byte aligned base and strides; any
+ * Hq that is a multiple of Hkv; o: same shape, bf16 (8-byte aligned) or f32
+ * (16-byte); lse: [B, Hq, N, 1] fp32 or ptr NULL.  start, count as for append.
+ * The logits are fp32 sums of exact products of q and the codes; softmax
+ * weights enter the product with V in fp16 with fp32 sums.  Up to 32 rows
+ * (N * Hq / Hkv) run on mma.sync and read each code once; more run on tcgen05.
+ * Results do not depend on what else runs: the split of the keys over the GPU
+ * is fixed by the lengths, and partial results merge in a fixed order.
+ * workspace: rcx_attn_kv_block_workspace_size(q, cache) bytes, 256-byte
+ * aligned, caller-owned, in any state; calls that may overlap need one each.
+ */
+int64_t rcx_attn_kv_block_workspace_size(rcx_tensor q, const rcx_kv_blocks* cache);
+int rcx_attn_kv_block_fwd(rcx_tensor q, const rcx_kv_blocks* cache, const int64_t* start, const int64_t* count,
+                          rcx_tensor o, rcx_tensor lse, int64_t window, int64_t n_sink, double temperature,
+                          void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
  * rcx_merge_partials -- LSE-weighted merge of two partial results over
  * disjoint key sets: m = max(lse_a, lse_b), w = exp(lse - m),
  * o = (w_a o_a + w_b o_b) / (w_a + w_b), lse = m + ln(w_a + w_b).
@@ -360,8 +487,9 @@ int rcx_release_staging(void);
 
 /*
  * Device status word: kernels with bounded waits record the first
- * RCX_ERR_DEVICE_TIMEOUT here instead of hanging.  rcx_device_status()
- * synchronises `stream`, stores the word in *status_out and clears it.
+ * RCX_ERR_DEVICE_TIMEOUT here instead of hanging, and the calls on
+ * rcx_kv_blocks record RCX_ERR_DEVICE_INDEX.  rcx_device_status() synchronises
+ * `stream`, stores the word in *status_out and clears it.
  */
 int rcx_device_status(void* stream, int* status_out);
 
@@ -381,11 +509,11 @@ int rcx_debug_inject_wait_timeout(int64_t spins);
  * CUDA objects (no device memory); the pool is kept until process exit.
  */
 typedef enum {
-    RCX_KERNEL_ROPE = 0,       /* rope_apply                   */
-    RCX_KERNEL_ATTN_TC = 1,    /* tcgen05 bf16 attention       */
+    RCX_KERNEL_ROPE = 0,       /* rope_apply, rope_axes_apply  */
+    RCX_KERNEL_ATTN_TC = 1,    /* tcgen05 attention            */
     RCX_KERNEL_ATTN_SIMT = 2,  /* SIMT fp32 attention          */
     RCX_KERNEL_MERGE = 3,      /* merge_partials               */
-    RCX_KERNEL_DECODE = 4,     /* decode attention + combine   */
+    RCX_KERNEL_DECODE = 4,     /* decode attention + combine, KV cache */
     RCX_KERNEL_KINDS = 5
 } rcx_kernel_kind;
 

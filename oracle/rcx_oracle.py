@@ -378,6 +378,103 @@ def dequantize_kv_int8(codes, scale):
 
 
 # --------------------------------------------------------------------------
+# Rotation by several axes
+# --------------------------------------------------------------------------
+
+def rope_axes_map(sections, interleaved: bool = False):
+    """Axis of each pair when axis a owns sections[a] pairs, one section after
+    another or (interleaved) in turn, skipping the axes that have run out."""
+    if not interleaved:
+        return [a for a, n in enumerate(sections) for _ in range(n)]
+    turns = [(i, a) for a, n in enumerate(sections) for i in range(n)]
+    return [a for _, a in sorted(turns)]
+
+
+def rope_rotate_axes(x, positions, inv_freq, axis, halves: bool, inverse: bool = False):
+    """x [N, H, d] rotated by positions [axes, N]: pair i turns by
+    positions[axis[i]] * inv_freq[i]; pair (i, i + d/2) (halves) or (2i, 2i + 1).
+    ("Context Extension" concept page, Technical principles, per axis.)"""
+    x = np.asarray(x, dtype=np.float64)
+    half = x.shape[-1] // 2
+    out = np.empty_like(x)
+    for i in range(half):
+        a, b = (i, i + half) if halves else (2 * i, 2 * i + 1)
+        phi = np.asarray(positions[axis[i]], dtype=np.float64)[:, None] * float(inv_freq[i])
+        z = (x[..., a] + 1j * x[..., b]) * np.exp((-1j if inverse else 1j) * phi)
+        out[..., a], out[..., b] = z.real, z.imag
+    return out
+
+
+# --------------------------------------------------------------------------
+# Block-scaled 8-bit KV cache
+# --------------------------------------------------------------------------
+
+def kv_code_values(y, kind: str):
+    """The code value nearest to y (ties to even): int8 in [-127, 127], e4m3 in
+    [-448, 448] (3 fraction bits, subnormals in steps of 2^-9)."""
+    y = np.asarray(y, dtype=np.float64)
+    if kind == "int8":
+        return np.clip(np.rint(y), -127, 127)
+    _, e = np.frexp(y)
+    step = np.exp2(np.maximum(e - 4, -9).astype(np.float64))
+    return np.clip(np.rint(y / step) * step, -448, 448)
+
+
+def kv_block_scale(amax: float, kind: str) -> float:
+    """Scale of a block whose largest magnitude is amax, a value fp32 holds.
+
+    int8: fl32(amax / 127), at least 2^-120; e4m3: the smallest power of two s
+    in [2^-120, 2^120] with amax <= 448 s; 0 for 0, NaN for a non-finite amax.
+    ("Context window extension: 4K to 1M" section 6.1: the cache in 8 bits; the
+    pages fix no format.)"""
+    if not math.isfinite(amax):
+        return math.nan
+    if amax == 0:
+        return 0.0
+    if kind == "int8":
+        return max(float(np.float32(amax / 127.0)), 2.0 ** -120)
+    s = 2.0 ** -120
+    while amax > 448 * s and s < 2.0 ** 120:
+        s *= 2
+    return s
+
+
+def kv_block_append(codes, scale, row, x, start: int, kind: str):
+    """Append x [n, d] (one sequence, one head, K or V) from token `start` on.
+
+    codes: code values [n_blocks, block, d] float64; scale: [n_blocks]; both
+    changed in place; row: the sequence's block numbers.  Blocks one by one:
+    the new scale is the larger of the old (if the block holds tokens) and the
+    new tokens'; old codes go to a larger scale as code * fl32(s_old / s), new
+    ones are x * fl32(1 / s), each rounded once."""
+    block, n = codes.shape[1], len(x)
+    t = start
+    while t < start + n:
+        p, lo = row[t // block], t % block
+        hi = min(block, lo + start + n - t)
+        new = np.asarray(x[t - start:t - start + hi - lo], dtype=np.float64)
+        s = kv_block_scale(float(np.abs(new).max()) if np.isfinite(new).all() else math.inf, kind)
+        if lo:
+            old = float(scale[p])
+            if not (math.isnan(s) or math.isnan(old)) and s > old:
+                codes[p, :lo] = kv_code_values(codes[p, :lo] * float(np.float32(old / s)), kind)
+            s = math.nan if math.isnan(s) or math.isnan(old) else max(s, old)
+        if s > 0:
+            codes[p, lo:hi] = kv_code_values(new * float(np.float32(1.0 / s)), kind)
+        else:
+            codes[p, lo:hi] = 0.0
+        scale[p] = s
+        t += hi - lo
+
+
+def kv_block_tokens(codes, scale, row, n: int):
+    """The first n tokens [n, d] of a sequence (one head, K or V): code * scale."""
+    block = codes.shape[1]
+    return np.stack([codes[row[t // block], t % block] * float(scale[row[t // block]]) for t in range(n)]) \
+        if n else np.zeros((0, codes.shape[2]))
+
+
+# --------------------------------------------------------------------------
 # Ring order
 # --------------------------------------------------------------------------
 

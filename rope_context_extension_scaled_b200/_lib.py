@@ -18,11 +18,12 @@ import torch
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "librcx.so")
 
-RCX_OK, RCX_ERR_INVALID_ARG, RCX_ERR_UNSUPPORTED, RCX_ERR_ALIGNMENT, RCX_ERR_CUDA, RCX_ERR_DEVICE_TIMEOUT = \
-    0, -1, -2, -3, -4, -5
-RCX_F32, RCX_BF16, RCX_I8 = 0, 1, 2
+RCX_OK, RCX_ERR_INVALID_ARG, RCX_ERR_UNSUPPORTED, RCX_ERR_ALIGNMENT, RCX_ERR_CUDA, RCX_ERR_DEVICE_TIMEOUT, \
+    RCX_ERR_DEVICE_INDEX = 0, -1, -2, -3, -4, -5, -6
+RCX_F32, RCX_BF16, RCX_I8, RCX_E4M3 = 0, 1, 2, 3
 PLAIN, PI, NTK, DYN_NTK, NTK_PARTS, YARN = range(6)
 ROTATE_Q, ROTATE_K = 1, 2
+ROPE_HALVES, ROPE_INVERSE = 1, 2
 
 # every symbol include/rcx.h declares
 EXPORTS = (
@@ -33,6 +34,8 @@ EXPORTS = (
     "rcx_ring_attn_fwd_noalloc", "rcx_rope_freqs_per_pair", "rcx_attn_decode_workspace_size",
     "rcx_attn_decode_fwd", "rcx_kv_quantize_int8", "rcx_attn_decode_int8_workspace_size",
     "rcx_attn_decode_int8_fwd", "rcx_attn_blockwise_merge_fwd", "rcx_release_staging",
+    "rcx_rope_axes_map", "rcx_rope_axes_apply", "rcx_kv_block_append", "rcx_kv_block_read",
+    "rcx_attn_kv_block_workspace_size", "rcx_attn_kv_block_fwd",
 )
 NOALLOC_SCRATCH_BYTES = 32 << 20   # RCX_NOALLOC_SCRATCH_BYTES in include/rcx.h
 KERNEL_KINDS = {"rope_apply": 0, "attn_tc": 1, "attn_simt": 2, "merge": 3, "decode": 4}
@@ -47,6 +50,12 @@ class RcxError(RuntimeError):
 class RcxTensor(ctypes.Structure):
     _fields_ = [("ptr", ctypes.c_void_p), ("dtype", ctypes.c_int32),
                 ("shape", ctypes.c_int64 * 4), ("stride", ctypes.c_int64 * 4)]
+
+
+class RcxKvBlocks(ctypes.Structure):
+    _fields_ = [("k", RcxTensor), ("v", RcxTensor), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("table", ctypes.c_void_p), ("B", ctypes.c_int64), ("width", ctypes.c_int64),
+                ("table_stride", ctypes.c_int64)]
 
 
 _lib = None
@@ -85,6 +94,15 @@ def load():
     lib.rcx_attn_blockwise_merge_fwd.argtypes = [T, T, T, T, T, T, T, i64, i64, i64, f64, i64, i64, vp, i64, pd,
                                                  ctypes.c_int, vp]
     lib.rcx_attn_blockwise_merge_fwd.restype = ctypes.c_int
+    C = ctypes.POINTER(RcxKvBlocks)
+    lib.rcx_rope_axes_map.argtypes = [ctypes.POINTER(i64), ctypes.c_int, ctypes.c_int, ctypes.c_int,
+                                      ctypes.POINTER(ctypes.c_int32)]
+    lib.rcx_rope_axes_apply.argtypes = [T, T, T, T, vp, ctypes.c_int, i64, i64, vp, vp, ctypes.c_int, vp]
+    lib.rcx_kv_block_append.argtypes = [T, T, C, vp, vp, vp]
+    lib.rcx_kv_block_read.argtypes = [C, vp, T, T, vp]
+    lib.rcx_attn_kv_block_workspace_size.argtypes = [T, C]
+    lib.rcx_attn_kv_block_workspace_size.restype = i64
+    lib.rcx_attn_kv_block_fwd.argtypes = [T, C, vp, vp, T, T, i64, i64, f64, vp, i64, vp]
     lib.rcx_release_staging.argtypes = []
     lib.rcx_release_staging.restype = ctypes.c_int
     lib.rcx_merge_partials.argtypes = [T, T, T, T, T, T, vp]
@@ -101,7 +119,8 @@ def load():
     for name in ("rcx_rope_freqs", "rcx_rope_apply", "rcx_attn_blockwise_fwd", "rcx_merge_partials",
                  "rcx_ring_attn_fwd", "rcx_ring_attn_fwd_host", "rcx_device_status",
                  "rcx_debug_inject_wait_timeout", "rcx_stats_enable_timing", "rcx_stats_reset",
-                 "rcx_stats_read"):
+                 "rcx_stats_read", "rcx_rope_axes_map", "rcx_rope_axes_apply", "rcx_kv_block_append",
+                 "rcx_kv_block_read", "rcx_attn_kv_block_fwd"):
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -123,6 +142,8 @@ def _dtype_code(t: torch.Tensor):
         return RCX_BF16
     if t.dtype == torch.int8:
         return RCX_I8
+    if t.dtype == torch.float8_e4m3fn:
+        return RCX_E4M3
     raise TypeError(f"unsupported dtype {t.dtype}")
 
 
@@ -404,4 +425,177 @@ def attn_decode_fwd(q, k, v, o=None, lse=None, window=0, n_sink=0, temperature=1
                                     float(temperature), int(q_index), pp, npos, fp, int(rope_flags),
                                     ctypes.c_void_p(workspace.data_ptr()), workspace.numel(), _stream(q.device))
     _check(st, "rcx_attn_decode_fwd")
+    return o, lse
+
+
+# ------------------------------------------------- rotation by several axes
+
+_DTYPES = {torch.float32: RCX_F32, torch.bfloat16: RCX_BF16, torch.int8: RCX_I8, torch.float8_e4m3fn: RCX_E4M3}
+_NULL = RcxTensor()
+
+
+def _view4(t):
+    """view() of a tensor that the caller knows to be there, in one construction."""
+    if t.dim() != 4:
+        raise ValueError("expected a 4-D [B, N, H, d] tensor")
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {t.dtype}")
+    return RcxTensor(t.data_ptr(), code, tuple(t.shape), t.stride())
+
+
+def _one_device(first, *rest):
+    """The CUDA device that all tensors (None: left out) are on."""
+    dev = first.device
+    if dev.type != "cuda":
+        raise ValueError(f"expected CUDA tensors, got one on {dev}")
+    for t in rest:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors on different devices: {dev} and {t.device}")
+    return dev
+
+
+def _call(fn, dev, *args):
+    """fn(*args, current stream of dev) with dev current."""
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    return fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+
+
+def _per_sequence(t, name, B, dev):
+    """Pointer of a contiguous int64 [B] tensor on dev (None: a null pointer)."""
+    if t is None:
+        return None
+    if t.dtype != torch.int64 or t.dim() != 1 or t.shape[0] != B or (B > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be a contiguous int64 [{B}] tensor")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, the other tensors on {dev}")
+    return t.data_ptr()
+
+
+def rope_axes_map(sections, interleaved=False):
+    """The axis of each pair (int32 [sum(sections)]) when axis a owns sections[a]
+    pairs: one section after another, or dealt out in turn (interleaved)."""
+    sec = [int(x) for x in sections]
+    out = np.zeros(max(sum(sec), 0), dtype=np.int32)
+    st = load().rcx_rope_axes_map((ctypes.c_int64 * max(len(sec), 1))(*sec), len(sec), int(bool(interleaved)), out.size,
+                                  out.ctypes.data_as(ctypes.POINTER(ctypes.c_int32)))
+    _check(st, "rcx_rope_axes_map")
+    return out
+
+
+def rope_axes_apply(q, k, inv_freq, axis, positions, halves=False, inverse=False, q_out=None, k_out=None):
+    """Rotate q and/or k (either may be None) by positions on several axes.
+
+    Pair i turns by positions[axis[i], b, n] * inv_freq[i]; the pair is (i, i + d/2)
+    with halves, else (2i, 2i + 1); inverse turns back, which is the gradient of
+    the rotation.  inv_freq [d/2] and axis [d/2] are host arrays, positions an
+    int64 [axes, B, N] tensor (axis and batch strides are free, 0 included).
+    Default: in place."""
+    if q is None and k is None:
+        return None, None
+    q_out = q if q_out is None else q_out
+    k_out = k if k_out is None else k_out
+    ref = q if q is not None else k
+    B, N, _, d = ref.shape
+    if positions.dtype != torch.int64 or positions.dim() != 3 or tuple(positions.shape[1:]) != (B, N):
+        raise ValueError(f"positions must be an int64 [axes, {B}, {N}] tensor")
+    if N > 1 and positions.stride(2) != 1:
+        raise ValueError("positions must have unit stride over tokens")
+    inv = np.ascontiguousarray(inv_freq, dtype=np.float64)
+    ax = np.ascontiguousarray(axis, dtype=np.int32)
+    if inv.shape != (d // 2,) or ax.shape != (d // 2,):
+        raise ValueError("inv_freq and axis need d/2 entries")
+    dev = _one_device(ref, positions, k, k_out if k is not None else None, q_out if q is not None else None)
+    nq, nk = q is None, k is None
+    st = _call(load().rcx_rope_axes_apply, dev, _NULL if nq else _view4(q), _NULL if nk else _view4(k),
+               _NULL if nq else _view4(q_out), _NULL if nk else _view4(k_out), positions.data_ptr(),
+               positions.shape[0], positions.stride(0), positions.stride(1), inv.ctypes.data, ax.ctypes.data,
+               (ROPE_HALVES if halves else 0) | (ROPE_INVERSE if inverse else 0))
+    _check(st, "rcx_rope_axes_apply")
+    return q_out, k_out
+
+
+# ------------------------------------------------- block-scaled 8-bit KV cache
+
+class KvBlockCache:
+    """A paged KV cache in 8 bits with one scale per block and head (rcx_kv_blocks).
+
+    k, v: code pools [n_blocks, block, Hkv, d], int8 or float8_e4m3fn; block 16,
+    32, 64 or 128; d 64 or 128; any strides with unit stride over d (the pools
+    may be stored [n_blocks, Hkv, block, d]).  k_scale, v_scale: contiguous
+    float32 [n_blocks, Hkv].  table: int32 [B, width], the block of each
+    sequence's tokens j * block ..; entries behind a sequence's tokens are not
+    read.  The handle keeps the tensors, not their contents: tables and pools
+    are the caller's to fill and to change between calls."""
+
+    def __init__(self, k, v, k_scale, v_scale, table):
+        n, _, h, _ = k.shape
+        for s in (k_scale, v_scale):
+            if not s.is_contiguous() or s.dtype != torch.float32 or tuple(s.shape) != (n, h):
+                raise ValueError(f"scales must be contiguous float32 [{n}, {h}] tensors")
+        if table.dtype != torch.int32 or table.dim() != 2 or (table.shape[1] > 1 and table.stride(1) != 1):
+            raise ValueError("table must be an int32 [B, width] tensor with unit stride over blocks")
+        self.device = _one_device(k, v, k_scale, v_scale, table)
+        self.k, self.v, self.k_scale, self.v_scale, self.table = k, v, k_scale, v_scale, table
+        self.view = RcxKvBlocks(_view4(k), _view4(v), k_scale.data_ptr(), v_scale.data_ptr(), table.data_ptr(),
+                                table.shape[0], table.shape[1], table.stride(0))
+        self._ref = ctypes.byref(self.view)
+
+
+def kv_block_append(k, v, cache, start, count=None):
+    """Quantise tokens start[b] .. start[b] + count[b] - 1 (rows of k, v [B, N, Hkv,
+    d], bf16 or fp32; count None: N each) into the cache's blocks."""
+    dev = _one_device(cache.k, k, v)
+    B = k.shape[0]
+    st = _call(load().rcx_kv_block_append, dev, _view4(k), _view4(v), cache._ref,
+               _per_sequence(start, "start", B, dev), _per_sequence(count, "count", B, dev))
+    _check(st, "rcx_kv_block_append")
+
+
+def kv_block_read(cache, lengths, n, dtype=torch.bfloat16, k_out=None, v_out=None):
+    """The first n tokens of each sequence as k, v [B, n, Hkv, d] in dtype (bf16 or
+    fp32), zeros from token lengths[b] on."""
+    B, (_, _, H, d) = cache.table.shape[0], cache.k.shape
+    dev = cache.device
+    if k_out is None:
+        k_out = torch.empty(B, n, H, d, dtype=dtype, device=dev)
+    if v_out is None:
+        v_out = torch.empty(B, n, H, d, dtype=dtype, device=dev)
+    _one_device(cache.k, k_out, v_out)
+    if k_out.shape[1] != n:
+        raise ValueError(f"outputs must hold n = {n} tokens")
+    st = _call(load().rcx_kv_block_read, dev, cache._ref, _per_sequence(lengths, "lengths", B, dev), _view4(k_out),
+               _view4(v_out))
+    _check(st, "rcx_kv_block_read")
+    return k_out, v_out
+
+
+def attn_kv_block_workspace_size(q, cache):
+    n = load().rcx_attn_kv_block_workspace_size(_view4(q), cache._ref)
+    if n < 0:
+        raise RcxError(RCX_ERR_INVALID_ARG, "rcx_attn_kv_block_workspace_size")
+    return int(n)
+
+
+def attn_kv_block_fwd(q, cache, start, count=None, o=None, lse=None, window=0, n_sink=0, temperature=1.0,
+                      workspace=None, want_lse=True):
+    """Attention of tokens start[b] .. start[b] + count[b] - 1 (rows of q [B, N, Hq,
+    d], bf16, rotated; count None: N each) over the cache, which holds them.
+
+    Rows from count[b] on give O = 0, lse = -inf.  workspace: uint8 tensor of
+    attn_kv_block_workspace_size(q, cache) bytes (None: a new one)."""
+    dev = _one_device(cache.k, q, o, lse, workspace)
+    B, N, H, _ = q.shape
+    if o is None:
+        o = torch.empty_like(q, memory_format=torch.contiguous_format)
+    if lse is None and want_lse:
+        lse = torch.empty(B, H, N, dtype=torch.float32, device=dev)
+    if workspace is None:
+        workspace = torch.empty(max(attn_kv_block_workspace_size(q, cache), 256), dtype=torch.uint8, device=dev)
+    st = _call(load().rcx_attn_kv_block_fwd, dev, _view4(q), cache._ref, _per_sequence(start, "start", B, dev),
+               _per_sequence(count, "count", B, dev), _view4(o), lse_view(lse), int(window), int(n_sink),
+               float(temperature), workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    _check(st, "rcx_attn_kv_block_fwd")
     return o, lse

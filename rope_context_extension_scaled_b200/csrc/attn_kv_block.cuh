@@ -1,0 +1,530 @@
+// Attention of a few query rows (one token, or a few drafted tokens, of each
+// sequence) over a block-scaled 8-bit paged KV cache, and the merge of partials.
+//
+// Key j of KV head h stands for k_code[j] * k_scale[block(j), h] (and likewise
+// V).  For every row:  x_j = (q . k_code_j) * k_scale * log2(e) / (sqrt(d) t),
+// p_j = 2^(x_j - m), O = sum p_j v_code_j v_scale / sum p_j, LSE = ln 2 (m +
+// log2 sum p_j).  Memory-bound: every code and scale a row sees is read once
+// per (sequence, KV head), for all its rows together.
+//
+// A warp takes 32-key tiles through a ring of cp.async stages and computes, per
+// 16 keys, S^T = K Q^T and O^T += V^T P^T on fp16 MMAs (m16n8k16, fp32
+// accumulators) with the keys (then the head dim) as MMA rows and the query
+// rows as the 8-wide columns, so no MMA row is padding.
+//  * Codes become exact fp16 by bit arithmetic (codes4_to_h2).  Each query row
+//    is scaled by a power of two to at most 2^15 and is then exact in fp16 too
+//    (down to 2^-28 of its largest element), so S is the fp32 sum of exact
+//    products: the logits carry no operand rounding.
+//  * The d order inside a dot product is free: lane (g, c) takes the 16-byte
+//    pieces c and c + 4 of key rows g and g + 8, and Q is laid out to match.
+//  * V^T comes from ldmatrix.trans over 16-bit elements (two dims of one key).
+//  * The block scale of K multiplies S per 16 keys (blocks are 16 tokens or
+//    more); that of V multiplies P as ratio to the largest V scale met so far.
+//    P is held as 2^7 p in fp16 (p <= 2^8 between moves of m), so weights down
+//    to 2^-31 of the largest keep their place; 11 bits of P against 8 of a
+//    bf16 output.
+//  * m moves only when a logit passes it by 2^8: most tiles need no shuffle
+//    and no rescale of O.
+// Table entries and scales come 16 tiles at a time, one per lane, a batch ahead.
+#pragma once
+#include "launch.h"
+#include "kv_int8.cuh"
+#include "kv_block_plan.cuh"
+
+namespace rcx {
+
+constexpr int kKbWarps = 4;
+constexpr int kKbStages = 3;
+constexpr int kKbKeys = kKvFewTile;             // keys per tile
+constexpr int kKbCtasPerSm = kKvFewCtasPerSm;
+constexpr float kKbLazy = 8.f;                  // log2 units a logit may pass m
+constexpr float kKbUp = 7.f;                    // P is held times 2^7
+
+template <int D>
+constexpr int kb_stage_bytes = 2 * kKbKeys * D;
+template <int D, int NT>
+constexpr int kb_smem_bytes = kKbWarps * kKbStages * kb_stage_bytes<D> + NT * (D / 16) * 32 * 8 + NT * 8 * 4;
+
+// 16-byte piece p of key row r sits at piece p ^ kb_swz(r): conflict-free for
+// the 8-row ldmatrix reads and for the quarter-warp reads of two rows.
+template <int D>
+__device__ __forceinline__ int kb_swz(int r) {
+  return D == 128 ? ((r & 1) << 2) | ((r >> 1) & 3) : (r >> 1) & 3;
+}
+
+// Power of two that brings a row of largest |element| `bits` (bf16 bits << 16)
+// into [2^14, 2^15), and its inverse; a row with infinities or NaN stays.
+__device__ __forceinline__ void row_pow2(uint32_t bits, float& up, float& down) {
+  const int eb = (int)(bits >> 23);
+  const int f = eb == 255 ? 127 : min(252, 268 - eb);
+  up = __uint_as_float((uint32_t)f << 23);
+  down = __uint_as_float((uint32_t)(254 - f) << 23);
+}
+
+// One output row piece of 4 dims (16-byte aligned in fp32, 8-byte in bf16).
+__device__ __forceinline__ void store_o4(const KvAttnArgs& a, int64_t off, float4 x) {
+  if (a.o_bf16)
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o.ptr) + off) = make_uint2(f2_to_bf2(x.x, x.y), f2_to_bf2(x.z, x.w));
+  else
+    *reinterpret_cast<float4*>(static_cast<float*>(a.o.ptr) + off) = x;
+}
+
+template <int D, int NT, int KIND>
+__global__ void __launch_bounds__(kKbWarps * 32, kKbCtasPerSm) attn_kv_block_kernel(const KvAttnArgs a) {
+  constexpr int LOGT = 5;
+  static_assert(1 << LOGT == kKbKeys, "tile");
+  constexpr int kChunks = D / 16;               // 16-dim MMA steps
+  constexpr int kStage = kb_stage_bytes<D>;
+  constexpr int kTile = kKbKeys * D;
+  constexpr int kPieces = D / 16;               // 16-byte pieces per key row
+  constexpr int kRowsPerCopy = 32 / kPieces;    // key rows one warp-wide 16-byte copy covers
+  constexpr bool kQRegs = NT <= 2;
+  extern __shared__ __align__(128) uint8_t kb_smem[];
+  __shared__ float sm_m[kKbWarps][NT * 8], sm_l[kKbWarps][NT * 8];
+  __shared__ PlanStart sm_plan;
+  uint2* sm_q = reinterpret_cast<uint2*>(kb_smem + kKbWarps * kKbStages * kStage);    // [NT][kChunks][32]
+  float* sm_fac = reinterpret_cast<float*>(sm_q + NT * kChunks * 32);                 // [NT * 8]
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int g = lane >> 2, c = lane & 3;
+  if (warp == 0) {
+    const PlanStart p = plan_start<LOGT>(a, blockIdx.x, lane);
+    if (lane == 0) sm_plan = p;
+  }
+  __syncthreads();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  SegWalk w;
+  w.init(sm_plan);
+  const KvBlockView& kv = a.c;
+  const int lb = kv.block_log2, bmask = (1 << lb) - 1;
+  uint8_t* wptr = kb_smem + warp * kKbStages * kStage;
+  const uint32_t wbuf = static_cast<uint32_t>(__cvta_generic_to_shared(wptr));
+
+  // copy lanes: row cr (+ kRowsPerCopy i), piece cp
+  const int cr = lane / kPieces, cp = lane % kPieces;
+  // fragment reads
+  const uint32_t k_frag = g * D + ((c ^ kb_swz<D>(g)) * 16);
+  const uint32_t v_row = ((lane & 7) + 8 * ((lane >> 3) & 1)) * D;
+  const int v_swz = kb_swz<D>(lane & 7), v_hi = lane >> 4;
+
+  while (w.next<LOGT>(a)) {
+    const Entry& t = w.t;
+    const int64_t b = t.b;
+    // ---- Q^T operand: chunk i of lane (g, c) holds dims base + {0, 2}, base + {1, 3}
+    // of row 8 nt + g, base = 16 c + 4 i (i < 4) or 64 + 16 c + 4 (i - 4)
+    for (int nt = warp; nt < NT; nt += kKbWarps) {
+      const int r = 8 * nt + g;
+      float x[4 * kChunks];
+      uint32_t mx = 0;
+      if (r < t.rows) {
+        const int n = r / a.G, h = r - n * a.G;
+        const __nv_bfloat16* qp = static_cast<const __nv_bfloat16*>(a.q.ptr) + b * a.q.sb + (int64_t)n * a.q.sn +
+                                  (int64_t)(w.hk * a.G + h) * a.q.sh + 16 * c;
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+          const uint2 u = *reinterpret_cast<const uint2*>(qp + (i < 4 ? 4 * i : 64 + 4 * (i - 4)));
+          const float2 lo = bf2_to_f2(u.x), hi = bf2_to_f2(u.y);
+          x[4 * i] = lo.x; x[4 * i + 1] = lo.y; x[4 * i + 2] = hi.x; x[4 * i + 3] = hi.y;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mx = max(mx, __float_as_uint(x[4 * i + e]) & 0x7fffffffu);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4 * kChunks; ++i) x[i] = 0.f;
+      }
+      mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      float up, down;
+      row_pow2(mx, up, down);
+#pragma unroll
+      for (int i = 0; i < kChunks; ++i)
+        sm_q[(nt * kChunks + i) * 32 + lane] =
+            make_uint2(f2_to_h2(x[4 * i] * up, x[4 * i + 2] * up), f2_to_h2(x[4 * i + 1] * up, x[4 * i + 3] * up));
+      if (c == 0) sm_fac[r] = down * a.scale_log2 * (KIND == 1 ? kE4m3Unscale : 1.f);
+    }
+    __syncthreads();
+    uint2 qf[kQRegs ? NT : 1][kChunks];
+    if constexpr (kQRegs) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) qf[nt][i] = sm_q[(nt * kChunks + i) * 32 + lane];
+    }
+    // per column (row of Q) 8 nt + 2 c + h: logit factor, token, running max, sum
+    float fac[NT][2], m[NT][2], l[NT][2];
+    int qi[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int r = 8 * nt + 2 * c + h;
+        fac[nt][h] = sm_fac[r];
+        qi[nt][h] = r < t.rows ? t.start + r / a.G : -1;
+        m[nt][h] = -INFINITY;
+        l[nt][h] = 0.f;
+      }
+    float o[kChunks][NT][4];
+#pragma unroll
+    for (int mt = 0; mt < kChunks; ++mt)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[mt][nt][e] = 0.f;
+    float vref = 0.f;                            // largest V scale met so far
+
+    // ---- this warp's tiles: u0 + warp, u0 + warp + kKbWarps, ...
+    const int ub = w.u0 + warp;
+    const int nk = ub < w.u1 ? (w.u1 - ub + kKbWarps - 1) / kKbWarps : 0;
+    const KeySpan span = t.span;
+    const int hi = span.hi;
+    const int32_t* trow = kv.table + b * kv.t_sb;
+    const float* ksh = kv.ks + w.hk;
+    const float* vsh = kv.vs + w.hk;
+    auto load_meta = [&](int batch, int& ph, float& ks, float& vs) {
+      ph = 0;
+      ks = vs = 0.f;
+      const int kk = 16 * batch + (lane >> 1);
+      if (kk < nk) {
+        const int key = (span.tile(ub + kKbWarps * kk) << LOGT) + ((lane & 1) << 4);
+        if (key < hi) {
+          int e = trow[key >> lb];
+          if ((unsigned)e >= (unsigned)kv.n_blocks) {
+            record_device_error(RCX_ERR_DEVICE_INDEX);
+            e = 0;
+          }
+          ph = e;
+          ks = ksh[(int64_t)e * kv.Hkv];
+          vs = vsh[(int64_t)e * kv.Hkv];
+          if (!(fabsf(vs) < INFINITY)) vs = __uint_as_float(0x7fffffffu);
+        }
+      }
+    };
+    const uint8_t* kb = kv.k + w.hk * kv.k_sh + cp * 16;
+    const uint8_t* vb = kv.v + w.hk * kv.v_sh + cp * 16;
+    int ph_a, ph_b;
+    float ks_a, vs_a, ks_b, vs_b;
+    load_meta(0, ph_a, ks_a, vs_a);
+    load_meta(1, ph_b, ks_b, vs_b);
+    auto issue = [&](int kk, int batch, int st) {
+      if (kk < nk) {
+        const int src = (kk >> 4) == batch ? ph_a : ph_b;
+        const int key0 = span.tile(ub + kKbWarps * kk) << LOGT;
+        const int rem = hi - key0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int ph = __shfl_sync(0xffffffffu, src, 2 * (kk & 15) + h);
+          const int64_t tok = ((key0 + 16 * h) & bmask) + cr;
+          const uint8_t* kp = kb + ph * kv.k_sb + tok * kv.k_sn;
+          const uint8_t* vp = vb + ph * kv.v_sb + tok * kv.v_sn;
+#pragma unroll
+          for (int i = 0; i < 16 / kRowsPerCopy; ++i) {
+            const int r = 16 * h + cr + kRowsPerCopy * i;
+            const uint32_t dst = wbuf + st * kStage + r * D + ((cp ^ kb_swz<D>(r & 7)) * 16);
+            const int bytes = r < rem ? 16 : 0;   // rows behind the keys: zeros, nothing read
+            const int64_t step = bytes ? (int64_t)kRowsPerCopy * i : -(int64_t)cr;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(kp + step * kv.k_sn), "r"(bytes)
+                         : "memory");
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + kTile), "l"(vp + step * kv.v_sn),
+                         "r"(bytes)
+                         : "memory");
+          }
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int s = 0; s < kKbStages - 1; ++s) issue(s, 0, s);
+
+    int st = 0;
+    for (int kk = 0; kk < nk; ++kk) {
+      const int batch = kk >> 4;
+      if ((kk & 15) == 0 && kk > 0) {
+        ph_a = ph_b;
+        ks_a = ks_b;
+        vs_a = vs_b;
+        load_meta(batch + 1, ph_b, ks_b, vs_b);
+      }
+      issue(kk + kKbStages - 1, batch, st == 0 ? kKbStages - 1 : st - 1);
+      asm volatile("cp.async.wait_group %0;" ::"n"(kKbStages - 1) : "memory");
+      __syncwarp();
+      const uint8_t* sk = wptr + st * kStage;
+      const int key0 = span.tile(ub + kKbWarps * kk) << LOGT;
+      float ks[2], vs[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        ks[u] = __shfl_sync(0xffffffffu, ks_a, 2 * (kk & 15) + u);
+        vs[u] = __shfl_sync(0xffffffffu, vs_a, 2 * (kk & 15) + u);
+      }
+      // S^T per 16-key half u: element e is (key 16 u + g + 8 (e >> 1), row 8 nt + 2 c + (e & 1))
+      float s[2][NT][4];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[u][nt][e] = 0.f;
+        uint32_t kw[2][kChunks];
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int hf = 0; hf < D / 64; ++hf) {
+            const uint4 x = *reinterpret_cast<const uint4*>(sk + (16 * u + 8 * r) * D + (k_frag ^ (64 * hf)));
+            kw[r][4 * hf] = x.x; kw[r][4 * hf + 1] = x.y; kw[r][4 * hf + 2] = x.z; kw[r][4 * hf + 3] = x.w;
+          }
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+          uint32_t af[4];
+          codes4_to_h2<KIND>(kw[0][i], af[0], af[2]);
+          codes4_to_h2<KIND>(kw[1][i], af[1], af[3]);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const uint2 q = kQRegs ? qf[kQRegs ? nt : 0][i] : sm_q[(nt * kChunks + i) * 32 + lane];
+            mma_f16_16816(s[u][nt], af, q.x, q.y);
+          }
+        }
+      }
+      // logits in log2 units; a tile cut by the mask or the keys' end element by element
+      const bool full = key0 + kKbKeys <= t.start + 1 + t.n_lo &&
+                        (a.window == 0 || key0 > t.start + t.n_hi - a.window || key0 + kKbKeys <= a.n_sink);
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const float f0 = fac[nt][0] * ks[u], f1 = fac[nt][1] * ks[u];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[u][nt][e] *= e & 1 ? f1 : f0;
+        }
+      if (!full) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int j = key0 + 16 * u + g + 8 * (e >> 1), i = qi[nt][e & 1];
+              if (!(j <= i && (a.window == 0 || j > i - a.window || j < a.n_sink))) s[u][nt][e] = -INFINITY;
+            }
+      }
+      bool move = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          move |= fmaxf(fmaxf(s[0][nt][h], s[0][nt][h + 2]), fmaxf(s[1][nt][h], s[1][nt][h + 2])) > m[nt][h] + kKbLazy;
+      const float vmax = fmaxf(vref, fmaxf(vs[0], vs[1]));   // NaN scales are passed over here
+      if (__any_sync(0xffffffffu, move) || vmax > vref) {
+        const float shrink = vmax > 0.f ? vref / vmax : 1.f;
+        vref = vmax;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float al[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float mx = fmaxf(fmaxf(s[0][nt][h], s[0][nt][h + 2]), fmaxf(s[1][nt][h], s[1][nt][h + 2]));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+            mx = fmaxf(mx, m[nt][h]);
+            const float alpha = mx == m[nt][h] ? 1.f : dec_exp2(m[nt][h] - mx);   // 0 from m = -inf
+            m[nt][h] = mx;
+            l[nt][h] *= alpha;
+            al[h] = alpha * shrink;
+          }
+#pragma unroll
+          for (int mt = 0; mt < kChunks; ++mt) {
+            o[mt][nt][0] *= al[0];
+            o[mt][nt][1] *= al[1];
+            o[mt][nt][2] *= al[0];
+            o[mt][nt][3] *= al[1];
+          }
+        }
+      }
+      const float inv_vref = vref > 0.f ? 1.f / vref : 0.f;
+      uint32_t pb[2][NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float mref[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) mref[h] = (m[nt][h] == -INFINITY ? 0.f : m[nt][h]) - kKbUp;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const float ratio = vs[u] * inv_vref;
+          float p[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            p[e] = dec_exp2(s[u][nt][e] - mref[e & 1]);
+            l[nt][e & 1] += p[e];
+            // a weight of zero takes nothing, not even NaN, from its block
+            p[e] = p[e] == 0.f ? 0.f : p[e] * ratio;
+          }
+          pb[u][nt][0] = movmatrix_t(f2_to_h2(p[0], p[1]));   // keys 2c, 2c + 1 of row 8 nt + g
+          pb[u][nt][1] = movmatrix_t(f2_to_h2(p[2], p[3]));   // keys 2c + 8, 2c + 9
+        }
+      }
+      // O^T += V^T P^T: MMA row g of m-tile mt is dim 16 mt + 2 g, row g + 8 is dim 16 mt + 2 g + 1
+      const uint32_t sv = wbuf + st * kStage + kTile + v_row;
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int mp = 0; mp < D / 32; ++mp) {
+          uint32_t rr[4];
+          ldsm_x4_t(rr, sv + 16 * u * D + (((2 * mp + v_hi) ^ v_swz) * 16));
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t af[4];
+            codes4_to_h2<KIND>(rr[2 * h], af[0], af[1]);
+            codes4_to_h2<KIND>(rr[2 * h + 1], af[2], af[3]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma_f16_16816(o[2 * mp + h][nt], af, pb[u][nt][0], pb[u][nt][1]);
+          }
+        }
+      __syncwarp();                              // the stage is refilled in the next iteration
+      st = st == kKbStages - 1 ? 0 : st + 1;
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+
+    // ---- merge the warps' states in shared memory (the stage buffers)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        l[nt][h] += __shfl_xor_sync(0xffffffffu, l[nt][h], 4);
+        l[nt][h] += __shfl_xor_sync(0xffffffffu, l[nt][h], 8);
+        l[nt][h] += __shfl_xor_sync(0xffffffffu, l[nt][h], 16);
+        if (g == 0) {
+          sm_m[warp][8 * nt + 2 * c + h] = m[nt][h];
+          sm_l[warp][8 * nt + 2 * c + h] = l[nt][h];
+        }
+      }
+    __syncthreads();
+    float* sm_o = reinterpret_cast<float*>(kb_smem);         // [warps][8 NT][D]
+    static_assert(kStage * kKbStages >= NT * 8 * D * 4, "merge area aliases the stage buffers");
+    const float unscale = vref * (KIND == 1 ? kE4m3Unscale : 1.f);
+#pragma unroll
+    for (int mt = 0; mt < kChunks; ++mt)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float* w0 = sm_o + (warp * NT * 8 + 8 * nt + 2 * c) * D + 16 * mt + 2 * g;
+        *reinterpret_cast<float2*>(w0) = make_float2(o[mt][nt][0] * unscale, o[mt][nt][2] * unscale);
+        *reinterpret_cast<float2*>(w0 + D) = make_float2(o[mt][nt][1] * unscale, o[mt][nt][3] * unscale);
+      }
+    __syncthreads();
+    const bool whole = w.whole();
+    const int64_t prow = ((int64_t)blockIdx.x * 2 + w.slot()) * a.rows_item;
+    for (int i = threadIdx.x; i < t.rows * (D / 4); i += kKbWarps * 32) {
+      const int r = i / (D / 4), dd = (i % (D / 4)) * 4;
+      float mm = -INFINITY;
+#pragma unroll
+      for (int x = 0; x < kKbWarps; ++x) mm = fmaxf(mm, sm_m[x][r]);
+      const float mr = mm == -INFINITY ? 0.f : mm;
+      float lt = 0.f;
+      float4 ot = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int x = 0; x < kKbWarps; ++x) {
+        const float wt = dec_exp2(sm_m[x][r] - mr);
+        const float4 y = *reinterpret_cast<const float4*>(sm_o + (x * NT * 8 + r) * D + dd);
+        lt += wt * sm_l[x][r];
+        ot.x += wt * y.x; ot.y += wt * y.y; ot.z += wt * y.z; ot.w += wt * y.w;
+      }
+      const float inv = lt == 0.f ? 0.f : 1.f / lt;
+      ot.x *= inv; ot.y *= inv; ot.z *= inv; ot.w *= inv;
+      const float lse = lt == 0.f ? -INFINITY : (mr - kKbUp + log2f(lt)) * 0.69314718055994530942f;
+      if (whole) {
+        const int n = r / a.G, hq = w.hk * a.G + r - n * a.G;
+        store_o4(a, b * a.o.sb + (int64_t)n * a.o.sn + (int64_t)hq * a.o.sh + dd, ot);
+        if (dd == 0 && a.lse) a.lse[b * a.lse_sb + hq * a.lse_sh + n] = lse;
+      } else {
+        *reinterpret_cast<float4*>(a.part_o + (prow + r) * D + dd) = ot;
+        if (dd == 0) a.part_lse[prow + r] = lse;
+      }
+    }
+    __syncthreads();                             // the buffers are free for the next segment
+  }
+}
+
+// Merge of items that several CTAs share, by the LSE rule of rcx_merge_partials,
+// and zeros (LSE -inf) for the rows of tokens past a sequence's count.  One CTA
+// per (entry, KV head) and slice of its rows; kWarpsPerRow warps share a row's
+// partials.  Waits for the attention kernel's end on the device (programmatic
+// dependent launch), so that its launch is hidden behind it.
+template <int D, int kWarpsPerRow>
+static __global__ void __launch_bounds__(256) attn_kv_block_merge_kernel(const KvAttnArgs a) {
+  constexpr int kL = D / 4;                      // lanes that hold dims (d = 64: half a warp)
+  __shared__ float sm_m[8], sm_l[8];
+  __shared__ float4 sm_o[8][32];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int e = blockIdx.x, hk = blockIdx.y;
+  const int E = a.B * a.n_rt;
+  const int T = a.prefix[E], p0 = a.prefix[e];
+  const int nt = (a.prefix[e + 1] - p0) / a.c.Hkv;
+  const int rt = a.n_rt == 1 ? 0 : e % a.n_rt;
+  const int64_t b = a.b0 + (a.n_rt == 1 ? e : e / a.n_rt);
+  const SeqRange s = seq_range(a.start, a.count, (int)b, a.N, a.c.cap);
+  const int r0 = rt * a.rows_item;
+  const int live = max(0, min(s.n * a.G - r0, a.rows_item));
+  const int rows = min(a.N * a.G - r0, a.rows_item);
+  const int i0 = p0 + hk * nt, i1 = i0 + nt;
+  const int c0 = nt > 0 ? range_owner(T, i0, a.n_cta) : 0, c1 = nt > 0 ? range_owner(T, i1 - 1, a.n_cta) : 0;
+  if (live == rows && c0 == c1) return;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int team = warp / kWarpsPerRow, sub = warp % kWarpsPerRow;
+  constexpr int kTeams = 8 / kWarpsPerRow;
+  const int dd = 4 * (lane % kL);
+  for (int rb = blockIdx.z * kTeams; rb < rows; rb += gridDim.z * kTeams) {
+    const int r = rb + team;
+    const bool row_ok = r < rows;
+    const int n = (r0 + r) / a.G, hq = hk * a.G + (r0 + r) - n * a.G;
+    const int64_t off = b * a.o.sb + (int64_t)n * a.o.sn + (int64_t)hq * a.o.sh + dd;
+    float mm = -INFINITY, lsum = 0.f;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    const bool shared = row_ok && r < live && c0 != c1;
+    if (shared) {
+      for (int c = c0 + sub; c <= c1; c += kWarpsPerRow) {
+        const int xc = range_start(T, c, a.n_cta);
+        if (xc == range_start(T, c + 1, a.n_cta)) continue;          // a CTA without tiles
+        const int64_t pr = ((int64_t)c * 2 + (xc >= i0 ? 0 : 1)) * a.rows_item + r;
+        const float ls = a.part_lse[pr];
+        const float4 y = *reinterpret_cast<const float4*>(a.part_o + pr * D + dd);
+        const float mn = fmaxf(mm, ls);                              // NaN stays in lsum and x
+        const float f0 = mm == mn ? 1.f : expf(mm - mn);
+        const float f1 = ls == -INFINITY ? 0.f : expf(ls - (mn == -INFINITY ? 0.f : mn));
+        x.x = x.x * f0 + f1 * y.x; x.y = x.y * f0 + f1 * y.y;
+        x.z = x.z * f0 + f1 * y.z; x.w = x.w * f0 + f1 * y.w;
+        lsum = lsum * f0 + f1;
+        mm = mn;
+      }
+    }
+    if constexpr (kWarpsPerRow > 1) {
+      if (lane == 0) {
+        sm_m[warp] = mm;
+        sm_l[warp] = lsum;
+      }
+      sm_o[warp][lane] = x;
+      __syncthreads();
+      if (sub == 0) {
+        float mt = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < kWarpsPerRow; ++i) mt = fmaxf(mt, sm_m[warp + i]);
+        x = make_float4(0.f, 0.f, 0.f, 0.f);
+        lsum = 0.f;
+#pragma unroll
+        for (int i = 0; i < kWarpsPerRow; ++i) {
+          const float f = sm_l[warp + i] == 0.f ? 0.f : expf(sm_m[warp + i] - (mt == -INFINITY ? 0.f : mt));
+          const float4 y = sm_o[warp + i][lane];
+          if (f != 0.f || sm_l[warp + i] != 0.f) {
+            x.x += f * y.x; x.y += f * y.y; x.z += f * y.z; x.w += f * y.w;
+            lsum += f * sm_l[warp + i];
+          }
+        }
+        mm = mt;
+      }
+      __syncthreads();
+    }
+    if (sub == 0 && row_ok && lane < kL && (shared || r >= live)) {
+      const float inv = lsum == 0.f ? 0.f : 1.f / lsum;
+      store_o4(a, off, make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv));
+      if (lane == 0 && a.lse) a.lse[b * a.lse_sb + hq * a.lse_sh + n] = lsum == 0.f ? -INFINITY : mm + logf(lsum);
+    }
+  }
+}
+
+}  // namespace rcx

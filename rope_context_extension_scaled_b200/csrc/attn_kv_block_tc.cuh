@@ -1,0 +1,573 @@
+// Tensor-core (tcgen05 / TMEM) attention of many query rows (drafts and prompt
+// chunks) over a block-scaled 8-bit paged KV cache, d = 64 or 128.
+//
+// Mathematics, mask and fp16 operands as in attn_kv_block.cuh: exact fp16 codes
+// and power-of-two scaled queries, so S is the fp32 sum of exact products; P as
+// 2^7 p in fp16.  Compute-bound for prompt chunks.
+//
+// One CTA per SM, walking its segments of the shared line of key tiles
+// (kv_block_plan.cuh).  An item is 256 rows (token, head of the group) of one
+// KV head, two slots of 128 that share every K/V tile; flattening tokens and
+// heads fills the MMA's 128 rows at any group size.  512 threads:
+//   warps 0-3   softmax, Q load and epilogue of slot 0 (a thread per row)
+//   warps 4-7   the same of slot 1 (idle when an item has at most 128 rows)
+//   warps 8-11  converters: codes of the next tile come into registers while
+//               the current one is turned into fp16 and stored as
+//               128B-swizzled K and V tiles (two stages), so the cache is read
+//               as it is stored, through its table, and no copy of it is made
+//   warp  12    MMA issuer and TMEM owner (13-15 have nothing to do)
+// The softmax threads hold half a row of S beside packed weights: registers move
+// to them from the other warpgroups (setmaxnreg; 184, 96 and 40 a thread add up
+// to 64,512 of the launch's 65,536).
+// TMEM: S0 | S1 | O0 | O1, 128 columns each.  P overwrites the first half of its
+// S; O += P V takes P from TMEM.
+//  * d order: a word's codes leave codes4_to_h2 in the order 0, 2, 1, 3.  Q is
+//    stored in the same order, and O's columns are put back in the epilogue.
+//  * K scales multiply S in the softmax, one factor per 16 columns, inside the
+//    multiply-add that the exponential needs anyway.  V scales go into the fp16
+//    V tile as ratio to the largest met so far (one half-precision product per
+//    pair of codes in the converters, which have the time; 11 bits beside the
+//    8 of a bf16 output); when that grows, O shrinks by the same factor.
+//    A non-finite V scale counts as zero there and marks its 16 keys; a row
+//    that sees a marked key ends as NaN, and no other row does.
+// Every mbarrier wait is bounded, as in attn_tc.cuh.
+#pragma once
+#include <type_traits>
+#include "attn_tc.cuh"
+#include "attn_kv_block.cuh"
+
+namespace rcx {
+
+constexpr int kBtM = 128;                       // rows per slot
+constexpr int kBtN = kKvTcTile;                 // keys per tile
+constexpr int kBtLogN = 7;
+static_assert(1 << kBtLogN == kBtN && 2 * kBtM == kKvTcRows, "tile");
+constexpr int kBtThreads = 512;
+constexpr int kBtRegsSoftmax = 184, kBtRegsConv = 96, kBtRegsMma = 40;
+static_assert(128 * (2 * kBtRegsSoftmax + kBtRegsConv + kBtRegsMma) <= 512 * 128, "registers of the launch");
+constexpr int kBtConv = 8;                      // first converter warp
+constexpr int kBtMma = 12;
+constexpr int kBtStages = 2;
+constexpr int kBtMeta = 4;                      // ring of per-tile scales
+constexpr uint32_t kBtHalf = kBtM * 128;        // 128 rows x 64 fp16, one swizzled block
+
+// The fp16 V tile holds value * this / (256 for e4m3) / (largest V scale): at
+// most 127 * 2^8 or 1.75 * 2^15, as far from fp16's subnormals as it goes.
+template <int KIND>
+constexpr float kBtVUp = KIND == 0 ? 256.f : 32768.f;
+
+struct BtMeta {
+  float ks[8];                                  // K scale of each 16 keys
+  float vfac;                                   // O's factor before this tile is added
+  uint32_t vbad;                                // 16-key groups with a non-finite V scale
+  float vref;                                   // largest V scale so far
+  uint32_t pad;
+};
+
+template <int D>
+struct BtSmem {
+  static constexpr uint32_t tile = kBtHalf * (D / 64);
+  static constexpr uint32_t q = 0;
+  static constexpr uint32_t k = q + 2 * tile;
+  static constexpr uint32_t v = k + kBtStages * tile;
+  static constexpr uint32_t bar = v + kBtStages * tile;
+  static constexpr uint32_t meta = bar + 256;
+  static constexpr uint32_t total = meta + kBtMeta * sizeof(BtMeta) + 64 + 1024;   // + plan, alignment slack
+};
+
+// kind::f16 descriptor: fp16 A and B, fp32 accumulator, M = 128
+__host__ __device__ constexpr uint32_t idesc_f16(bool b_mn_major, int n) {
+  return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kBtM >> 4) << 24);
+}
+
+// (a, b) * f + c, the product rounded before the sum: the row maximum was rounded
+// the same way, so the winner's exponent is c + max exactly, however large the
+// logits.  (An unrounded product may pass the rounded maximum by half a step,
+// which from 2^25 on is more than fp16 weights hold.)
+__device__ __forceinline__ void mul_add2(float& r0, float& r1, float a, float b, float f, float c) {
+  r0 = __fadd_rn(__fmul_rn(a, f), c);
+  r1 = __fadd_rn(__fmul_rn(b, f), c);
+}
+
+template <int R>
+__device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
+template <int R>
+__device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
+
+template <int D, int KIND>
+__global__ void __launch_bounds__(kBtThreads, 1) attn_kv_block_tc_kernel(const __grid_constant__ KvAttnArgs a) {
+  using L = BtSmem<D>;
+  constexpr int kPieces = D / 16;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_addr(smem);
+  const uint32_t bar0 = sbase + L::bar;
+  auto BAR = [&](int i) { return bar0 + 8u * (uint32_t)i; };
+  enum {
+    B_QREADY = 0,                     // [2] Q rows of the slot stored (128 arrivals)
+    B_KFULL = 2,                      // [stages] (128 arrivals)
+    B_KEMPTY = B_KFULL + kBtStages,
+    B_VFULL = B_KEMPTY + kBtStages,
+    B_VEMPTY = B_VFULL + kBtStages,
+    B_SFULL = B_VEMPTY + kBtStages,   // [2]
+    B_PREADY = B_SFULL + 2,           // [2] (128 arrivals)
+    B_OFINAL = B_PREADY + 2,          // [2]
+    B_META = B_OFINAL + 2,            // [ring] scales of a tile written (32 arrivals)
+    B_DRAIN = B_META + kBtMeta,
+    B_NEVER,
+    B_COUNT
+  };
+  static_assert(8 * B_COUNT + 16 <= 256, "barrier area");
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::bar + 8 * B_COUNT);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::bar + 8 * B_COUNT + 8);
+  BtMeta* meta = reinterpret_cast<BtMeta*>(smem + L::meta);
+  PlanStart* plan = reinterpret_cast<PlanStart*>(smem + L::meta + kBtMeta * sizeof(BtMeta));
+
+  const int warp = threadIdx.x / 32;
+  const int lane = threadIdx.x % 32;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < B_COUNT; ++i) {
+      uint32_t cnt = 1;
+      if (i < 2 || (i >= B_KFULL && i < B_KFULL + kBtStages) || (i >= B_VFULL && i < B_VFULL + kBtStages) ||
+          i == B_PREADY || i == B_PREADY + 1)
+        cnt = 128;
+      if (i >= B_META && i < B_META + kBtMeta) cnt = 32;
+      mbar_init(BAR(i), cnt);
+    }
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    fence_proxy_async_smem();
+  }
+  if (warp == 0) {
+    const PlanStart p = plan_start<kBtLogN>(a, blockIdx.x, lane);
+    if (lane == 0) *plan = p;
+  }
+  if (warp == kBtMma) tmem_alloc(smem_addr(tmem_slot), 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const uint32_t tmem = *tmem_slot;
+  auto tS = [&](int s) { return tmem + 128u * (uint32_t)s; };
+  auto tO = [&](int s) { return tmem + 256u + 128u * (uint32_t)s; };
+  auto warp_wait = [&](int b, uint32_t par) { return __all_sync(0xffffffffu, mbar_wait(BAR(b), par, abort_flag)); };
+  SegWalk w;
+  w.init(*plan);
+  bool ok = true;
+
+  if (warp >= kBtMma) {
+    regs_down<kBtRegsMma>();
+    if (warp == kBtMma) {
+    // ================================================================ MMA issuer
+    constexpr uint32_t id_qk = idesc_f16(false, kBtN);
+    constexpr uint32_t id_pv = idesc_f16(true, D);
+    const uint32_t d_hi = (uint32_t)(sw128_desc(sbase, 16, 1024) >> 32);
+    const uint32_t q_lo = (uint32_t)sw128_desc(sbase + L::q, 16, 1024);
+    const uint32_t k_lo = (uint32_t)sw128_desc(sbase + L::k, 16, 1024);
+    const uint32_t v_lo = (uint32_t)sw128_desc(sbase + L::v, kBtHalf, 1024);
+    auto issue_s = [&](int s, int st) {
+      const uint32_t a0 = q_lo + s * (L::tile >> 4), b0 = k_lo + st * (L::tile >> 4);
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t off = ((kk / 4) * kBtHalf + (kk % 4) * 32) >> 4;
+        umma_ss_e(tS(s), a0 + off, b0 + off, d_hi, id_qk, kk > 0);
+      }
+    };
+    auto issue_pv = [&](int s, int st, bool first_tile) {
+      const uint32_t b0 = v_lo + st * (L::tile >> 4);
+#pragma unroll
+      for (int kk = 0; kk < kBtN / 16; ++kk)
+        umma_ts_e(tO(s), tS(s) + kk * 8, b0 + kk * (2048 >> 4), d_hi, id_pv, (!first_tile || kk > 0) ? 1u : 0u);
+    };
+    if (a.inject_spins > 0) {
+      // test hook: a wait that nothing ends
+      bool got = false;
+      if (lane == 0) {
+        for (int64_t i = 0; i < a.inject_spins && !got; ++i) got = mbar_test(BAR(B_NEVER), 0);
+        if (!got) {
+          *abort_flag = 1;
+          record_device_error(RCX_ERR_DEVICE_TIMEOUT);
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, got ? 1 : 0, 0) != 0;
+    }
+    int jg = 0, js[2] = {0, 0}, segs[2] = {0, 0};   // tiles so far (all, per slot), segments per slot
+    while (ok && w.next<kBtLogN>(a)) {
+      const int n = w.u1 - w.u0;
+      const int ns = w.t.rows > kBtM ? 2 : 1;
+      for (int s = 0; s < ns && ok; ++s) ok = warp_wait(B_QREADY + s, segs[s] & 1);
+      if (!ok) break;
+      {
+        const int st0 = jg % kBtStages;
+        if (!(ok = warp_wait(B_KFULL + st0, (jg / kBtStages) & 1))) break;
+        tc_fence_after();
+        for (int s = 0; s < ns; ++s) {
+          issue_s(s, st0);
+          umma_commit_e(BAR(B_SFULL + s));
+        }
+        umma_commit_e(BAR(B_KEMPTY + st0));
+      }
+      for (int j = 0; ok && j < n; ++j) {
+        const int g = jg + j;
+        const int st = g % kBtStages, st1 = (g + 1) % kBtStages;
+        const bool last = j == n - 1;
+        if (!(ok = warp_wait(B_VFULL + st, (g / kBtStages) & 1))) break;
+        for (int s = 0; s < ns; ++s) {
+          if (!(ok = warp_wait(B_PREADY + s, (js[s] + j) & 1))) break;
+          tc_fence_after();
+          issue_pv(s, st, j == 0);
+          if (last) umma_commit_e(BAR(B_OFINAL + s));
+          if (s == ns - 1) umma_commit_e(BAR(B_VEMPTY + st));
+          if (!last) {
+            if (s == 0) {
+              if (!(ok = warp_wait(B_KFULL + st1, ((g + 1) / kBtStages) & 1))) break;
+              tc_fence_after();
+            }
+            issue_s(s, st1);
+            umma_commit_e(BAR(B_SFULL + s));
+            if (s == ns - 1) umma_commit_e(BAR(B_KEMPTY + st1));
+          }
+        }
+      }
+      jg += n;
+      for (int s = 0; s < ns; ++s) {
+        js[s] += n;
+        ++segs[s];
+      }
+    }
+    // all MMAs issued complete before TMEM is released
+    umma_commit_e(BAR(B_DRAIN));
+    if (lane == 0) mbar_wait(BAR(B_DRAIN), 0, abort_flag, 100000000ull, false);
+    __syncwarp();
+    }
+  } else if (warp >= kBtConv) {
+    // ================================================================ converters
+    regs_down<kBtRegsConv>();
+    const int tid = threadIdx.x - kBtConv * 32;
+    const KvBlockView& kv = a.c;
+    const int lb = kv.block_log2, bmask = (1 << lb) - 1;
+    constexpr int kRows = 128 / kPieces;          // key rows the 128 threads cover at once
+    const int pr = tid / kPieces, pc = tid % kPieces;
+    // a piece of 16 codes becomes two 16-byte chunks of one swizzled 128-byte row;
+    // pieces of the upper half store theirs in the other order (bank conflicts)
+    const int flip = (pc >> 2) & 1;
+    uint4 kr[kPieces], vr[kPieces];
+    int jg = 0;
+    float vref = 0.f;
+    while (ok && w.next<kBtLogN>(a)) {
+      const KeySpan span = w.t.span;
+      const int hi = span.hi;
+      const int32_t* trow = kv.table + (int64_t)w.t.b * kv.t_sb;
+      const uint8_t* kb = kv.k + w.hk * kv.k_sh + pc * 16;
+      const uint8_t* vb = kv.v + w.hk * kv.v_sh + pc * 16;
+      // lane i < 8: block of 16-key group i of tile u (0 behind the keys)
+      auto load_phys = [&](int u) {
+        int e = 0;
+        if (u < w.u1) {
+          const int key = (span.tile(u) << kBtLogN) + 16 * (lane & 7);
+          if (key < hi) {
+            e = trow[key >> lb];
+            if ((unsigned)e >= (unsigned)kv.n_blocks) {
+              record_device_error(RCX_ERR_DEVICE_INDEX);
+              e = 0;
+            }
+          }
+        }
+        return e;
+      };
+      // lanes 0-7 K, 8-15 V scale of the groups of tile u with blocks ph
+      auto load_scale = [&](int u, int ph) {
+        float s = 0.f;
+        if (u < w.u1 && lane < 16 && (span.tile(u) << kBtLogN) + 16 * (lane & 7) < hi)
+          s = (lane < 8 ? kv.ks : kv.vs)[(int64_t)ph * kv.Hkv + w.hk];
+        return s;
+      };
+      auto load_codes = [&](int u, int ph, const uint8_t* base, int64_t sb, int64_t sn, uint4* r) {
+        const int key0 = span.tile(u) << kBtLogN;
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+          const int row = i * kRows + pr;
+          const int phys = __shfl_sync(0xffffffffu, ph, row >> 4);
+          r[i] = make_uint4(0u, 0u, 0u, 0u);      // keys behind the sequence: zeros, nothing read
+          if (key0 + row < hi)
+            r[i] = __ldg(reinterpret_cast<const uint4*>(base + phys * sb + ((key0 + row) & bmask) * sn));
+        }
+      };
+      auto store_tile = [&](uint32_t tile_off, const uint4* r, uint32_t ratios, auto scaled) {
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+          const int row = i * kRows + pr;
+          const uint32_t wv[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
+          uint32_t h[8];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) codes4_to_h2<KIND>(wv[e], h[2 * e], h[2 * e + 1]);
+          if constexpr (decltype(scaled)::value) {
+            const uint32_t rb = __shfl_sync(0xffffffffu, ratios, 8 + (row >> 4));
+            const __half2 rh = *reinterpret_cast<const __half2*>(&rb);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const __half2 x = __hmul2(*reinterpret_cast<const __half2*>(&h[e]), rh);
+              h[e] = *reinterpret_cast<const uint32_t*>(&x);
+            }
+          }
+          uint8_t* dst = smem + tile_off + (pc >> 2) * kBtHalf + row * 128;
+          const int c0 = (2 * (pc & 3) + flip) ^ (row & 7);
+          const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi4 = make_uint4(h[4], h[5], h[6], h[7]);
+          *reinterpret_cast<uint4*>(dst + c0 * 16) = flip ? hi4 : lo;
+          *reinterpret_cast<uint4*>(dst + (c0 ^ 1) * 16) = flip ? lo : hi4;
+        }
+      };
+      int ph = load_phys(w.u0), ph_next = load_phys(w.u0 + 1);
+      float sc = load_scale(w.u0, ph);
+      load_codes(w.u0, ph, kb, kv.k_sb, kv.k_sn, kr);
+      load_codes(w.u0, ph, vb, kv.v_sb, kv.v_sn, vr);
+      vref = 0.f;
+      for (int u = w.u0; u < w.u1; ++u, ++jg) {
+        const int st = jg % kBtStages;
+        const uint32_t par = ((jg / kBtStages) & 1) ^ 1;
+        const int ph_next2 = load_phys(u + 2);
+        const float sc_next = load_scale(u + 1, ph_next);
+        // V scales: running maximum, ratios in fp16 (lanes 8-15 hold the groups')
+        const bool is_v = lane >= 8 && lane < 16;
+        const bool bad = is_v && !(fabsf(sc) < INFINITY);
+        const float sv = is_v && !bad ? sc : 0.f;
+        const float vmax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(sv, 0.f))));
+        const uint32_t vbad = (__ballot_sync(0xffffffffu, bad) >> 8) & 0xffu;
+        const float vnew = fmaxf(vref, vmax);
+        const float vfac = vnew > 0.f ? vref / vnew : 1.f;
+        vref = vnew;
+        const float ratio = vref > 0.f ? sv / vref * kBtVUp<KIND> : 0.f;
+        const uint32_t ratios = f2_to_h2(ratio, ratio);
+        if (!(ok = warp_wait(B_KEMPTY + st, par))) break;
+        store_tile(L::k + st * L::tile, kr, 0u, std::false_type{});
+        if (warp == kBtConv) {                    // the tile's scales
+          BtMeta* mt = meta + jg % kBtMeta;
+          if (lane < 8) mt->ks[lane] = sc;
+          if (lane == 8) {
+            mt->vfac = vfac;
+            mt->vbad = vbad;
+            mt->vref = vref;
+          }
+          mbar_arrive(BAR(B_META + jg % kBtMeta));
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(BAR(B_KFULL + st));
+        if (u + 1 < w.u1) load_codes(u + 1, ph_next, kb, kv.k_sb, kv.k_sn, kr);
+        if (!(ok = warp_wait(B_VEMPTY + st, par))) break;
+        store_tile(L::v + st * L::tile, vr, ratios, std::true_type{});
+        fence_proxy_async_smem();
+        mbar_arrive(BAR(B_VFULL + st));
+        if (u + 1 < w.u1) load_codes(u + 1, ph_next, vb, kv.v_sb, kv.v_sn, vr);
+        ph = ph_next;
+        ph_next = ph_next2;
+        sc = sc_next;
+      }
+    }
+  } else {
+    // ================================================================ softmax + epilogue
+    regs_up<kBtRegsSoftmax>();
+    const int s = warp / 4;                     // slot of this warpgroup
+    const int q4 = warp % 4;                    // TMEM lane quarter
+    const int r = q4 * 32 + lane;               // row within the slot
+    const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
+    int jg = 0, js = 0, segs = 0;
+    while (ok && w.next<kBtLogN>(a)) {
+      const int n = w.u1 - w.u0;
+      const int ns = w.t.rows > kBtM ? 2 : 1;
+      if (s >= ns) {
+        jg += n;
+        continue;
+      }
+      const Entry& t = w.t;
+      const int64_t b = t.b;
+      const bool row_ok = s * kBtM + r < t.rows;
+      const int rr = t.r0 + min(s * kBtM + r, t.rows - 1);     // rows behind the last repeat it
+      const int tok = rr / a.G, hq = w.hk * a.G + rr - tok * a.G;
+      const int gi = t.start + tok;
+      // ---- Q row -> power-of-two scaled fp16 in shared memory.  The buffer is free:
+      // the slot's last OFINAL came after every S MMA that read it.
+      float fac;
+      {
+        const uint4* qp = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q.ptr) + b * a.q.sb +
+                                                         (int64_t)tok * a.q.sn + (int64_t)hq * a.q.sh);
+        uint4 x[D / 8];
+        uint32_t mx = 0;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) x[i] = qp[i];
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          const uint32_t wv[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mx = max(mx, max(wv[e] & 0x7fff0000u, (wv[e] << 16) & 0x7fff0000u));
+        }
+        float up, down;
+        row_pow2(mx, up, down);
+        fac = down * a.scale_log2 * (KIND == 1 ? kE4m3Unscale : 1.f);
+        uint8_t* qrow = smem + L::q + s * L::tile + r * 128;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          const float2 f0 = bf2_to_f2(x[i].x), f1 = bf2_to_f2(x[i].y), f2 = bf2_to_f2(x[i].z), f3 = bf2_to_f2(x[i].w);
+          const uint4 h = make_uint4(f2_to_h2(f0.x * up, f1.x * up), f2_to_h2(f0.y * up, f1.y * up),
+                                     f2_to_h2(f2.x * up, f3.x * up), f2_to_h2(f2.y * up, f3.y * up));
+          *reinterpret_cast<uint4*>(qrow + (i >> 3) * kBtHalf + (((i & 7) ^ (r & 7)) * 16)) = h;
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(BAR(B_QREADY + s));
+      }
+      const int ti_lo = t.start + (t.r0 + s * kBtM) / a.G;
+      const int ti_hi = t.start + (t.r0 + min((s + 1) * kBtM, t.rows) - 1) / a.G;
+      float m_used = -INFINITY, l = 0.f, vref = 0.f, poison = 0.f;
+      for (int j = 0; j < n; ++j) {
+        const int key0 = w.t.span.tile(w.u0 + j) << kBtLogN;
+        const int g = jg + j;
+        // S first: its phases are counted per slot, and once tile g's S is there the
+        // ring's barrier stands at tile g (a slot that sat out segments would take an
+        // older phase of equal parity for it)
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(BAR(B_SFULL + s), (js + j) & 1, abort_flag) &&
+                                               mbar_wait(BAR(B_META + g % kBtMeta), (g / kBtMeta) & 1, abort_flag))))
+          break;
+        tc_fence_after();
+        const BtMeta* mt = meta + g % kBtMeta;
+        const bool full = key0 + kBtN <= ti_lo + 1 &&
+                          (a.window == 0 || key0 > ti_hi - a.window || key0 + kBtN <= a.n_sink);
+        auto clip = [](int x) { return x < -1 ? -1 : (x > kBtN ? kBtN : x); };
+        const int lim = clip(gi - key0);
+        const int win_lo = a.window > 0 ? clip(gi - a.window - key0) : -1;
+        const int snk = a.window > 0 ? clip(a.n_sink - 1 - key0) : -1;
+        const float vfac = mt->vfac;
+        vref = mt->vref;
+        if (const uint32_t vbad = mt->vbad) {   // NaN for the rows that see a marked key
+          for (int c = 0; c < kBtN; ++c)
+            if ((vbad >> (c >> 4)) & 1)
+              if (c <= lim && (c > win_lo || c <= snk)) poison = __uint_as_float(0x7fffffffu);
+        }
+        // 64 columns at a time: factors and mask, and the row maximum
+        auto load_half = [&](int hf, float* x, float& mx) {
+          uint32_t* u = reinterpret_cast<uint32_t*>(x);
+          tmem_ld32(tS(s) + lane_off + 64 * hf, u);
+          tmem_ld32(tS(s) + lane_off + 64 * hf + 32, u + 32);
+          tmem_wait_ld();
+          if (full) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              float m2[2] = {x[16 * q], x[16 * q + 1]};
+#pragma unroll
+              for (int c = 2; c < 16; c += 4) {
+                m2[0] = fmax3(m2[0], x[16 * q + c], c + 1 < 16 ? x[16 * q + c + 1] : m2[0]);
+                if (c + 2 < 16) m2[1] = fmax3(m2[1], x[16 * q + c + 2], x[16 * q + c + 3]);
+              }
+              mx = fmaxf(mx, fmaxf(m2[0], m2[1]) * (mt->ks[4 * hf + q] * fac));
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < 64; ++c) {
+              const int col = 64 * hf + c;
+              const bool vis = col <= lim && (col > win_lo || col <= snk);
+              x[c] = vis ? x[c] * (mt->ks[4 * hf + (c >> 4)] * fac) : -INFINITY;
+              mx = fmaxf(mx, x[c]);
+            }
+          }
+        };
+        float l2[2] = {0.f, 0.f};
+        // weights of a half, packed in pairs; their sum goes to l2
+        auto exp_half = [&](int hf, const float* x, float mref, uint32_t* pc) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const int c = 2 * i;
+            float p0, p1;
+            if (full) {
+              const float f = mt->ks[4 * hf + (c >> 4)] * fac;
+              mul_add2(p0, p1, x[c], x[c + 1], f, -mref);
+              p0 = fast_exp2(p0);
+              p1 = fast_exp2(p1);
+            } else {
+              p0 = fast_exp2(x[c] - mref);
+              p1 = fast_exp2(x[c + 1] - mref);
+            }
+            l2[i & 1] += p0 + p1;
+            pc[i] = f2_to_h2(p0, p1);
+          }
+        };
+        float mx = -INFINITY;
+        float x[64];
+        load_half(0, x, mx);
+        load_half(1, x, mx);
+        const float m_new = fmaxf(m_used, mx);
+        const bool need = m_new > m_used + kLazyRescale;
+        float alpha = 1.f;
+        if (need) {
+          alpha = fast_exp2(m_used - m_new);     // 0 when m_used = -inf
+          m_used = m_new;
+          l *= alpha;
+        }
+        const float mref = (m_used == -INFINITY ? 0.f : m_used) - kKbUp;
+        // P of columns 64..127 goes where S of columns 64..127 is done with but S of
+        // 32..63 still stands: it waits in registers until that half is read again
+        uint32_t p_hi[32], p_lo[32];
+        exp_half(1, x, mref, p_hi);
+        float again = -INFINITY;
+        load_half(0, x, again);
+        tmem_st32(tS(s) + lane_off + 32, p_hi);
+        exp_half(0, x, mref, p_lo);
+        tmem_st32(tS(s) + lane_off, p_lo);
+        l += l2[0] + l2[1];
+        const float of = alpha * vfac;
+        if (__any_sync(0xffffffffu, of != 1.f) && j > 0) {
+#pragma unroll 1
+          for (int cb = 0; cb < D / 32; ++cb) {
+            uint32_t o[32];
+            tmem_ld32(tO(s) + lane_off + cb * 32, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * of);
+            tmem_st32(tO(s) + lane_off + cb * 32, o);
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(BAR(B_PREADY + s));
+      }
+      if (!ok) break;
+
+      // ---- epilogue: O / l -> the output row, or a partial for the merge
+      if (!(ok = __all_sync(0xffffffffu, mbar_wait(BAR(B_OFINAL + s), segs & 1, abort_flag)))) break;
+      tc_fence_after();
+      const bool whole = w.whole();
+      const float lse = l == 0.f ? -INFINITY : (m_used - kKbUp + log2f(l)) * 0.69314718055994530942f;
+      const float inv = (l == 0.f ? 0.f : vref * ((KIND == 1 ? kE4m3Unscale : 1.f) / kBtVUp<KIND>) / l) + poison;
+      const int64_t prow = ((int64_t)blockIdx.x * 2 + w.slot()) * a.rows_item + s * kBtM + r;
+      const int64_t off = b * a.o.sb + (int64_t)tok * a.o.sn + (int64_t)hq * a.o.sh;
+#pragma unroll 1
+      for (int cb = 0; cb < D / 32; ++cb) {
+        uint32_t o[32];
+        tmem_ld32(tO(s) + lane_off + cb * 32, o);
+        tmem_wait_ld();
+        if (row_ok) {
+#pragma unroll
+          for (int c = 0; c < 32; c += 4) {     // columns hold dims 0, 2, 1, 3 of each four
+            const float4 y = make_float4(__uint_as_float(o[c]) * inv, __uint_as_float(o[c + 2]) * inv,
+                                         __uint_as_float(o[c + 1]) * inv, __uint_as_float(o[c + 3]) * inv);
+            if (whole) store_o4(a, off + 32 * cb + c, y);
+            else *reinterpret_cast<float4*>(a.part_o + prow * D + 32 * cb + c) = y;
+          }
+        }
+      }
+      if (row_ok) {
+        if (!whole) a.part_lse[prow] = lse;
+        else if (a.lse) a.lse[b * a.lse_sb + hq * a.lse_sh + tok] = lse;
+      }
+      tc_fence_before();                        // O is read before the next segment's MMAs write it (QREADY orders)
+      jg += n;
+      js += n;
+      ++segs;
+    }
+  }
+
+  // ---- teardown
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kBtMma) tmem_dealloc(tmem, 512);
+}
+
+}  // namespace rcx

@@ -1,0 +1,47 @@
+// Launchers of the tensor-core attention over the block-scaled KV cache
+// (attn_kv_block_tc.cuh) and of the merge of partials (attn_kv_block.cuh).
+#include "launch.h"
+#include "attn_kv_block_tc.cuh"
+
+namespace rcx {
+
+template <int D, int KIND>
+static int kb_tc_launch(const KvAttnArgs& a, cudaStream_t stream) {
+  auto kern = attn_kv_block_tc_kernel<D, KIND>;
+  if (allow_smem(kern, BtSmem<D>::total)) return RCX_ERR_CUDA;
+  kern<<<a.n_cta, kBtThreads, BtSmem<D>::total, stream>>>(a);
+  return launch_status();
+}
+
+int attn_kv_block_tc_launch(const KvAttnArgs& a, int kind, cudaStream_t stream) {
+  LaunchScope scope(RCX_KERNEL_ATTN_TC, stream);
+  if (a.q.D == 64) return kind == 0 ? kb_tc_launch<64, 0>(a, stream) : kb_tc_launch<64, 1>(a, stream);
+  return kind == 0 ? kb_tc_launch<128, 0>(a, stream) : kb_tc_launch<128, 1>(a, stream);
+}
+
+// Few rows: a CTA of eight warps per row (an item's partials may come from
+// every CTA); many rows: a warp per row (an item is cut once or twice).
+int attn_kv_block_merge_launch(const KvAttnArgs& a, cudaStream_t stream) {
+  LaunchScope scope(RCX_KERNEL_DECODE, stream);
+  const bool few = a.rows_item <= kKvFewRows;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(a.B * a.n_rt), (unsigned)a.c.Hkv, few ? (unsigned)(a.N * a.G) : 4u);
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  auto kern = a.q.D == 64 ? (few ? attn_kv_block_merge_kernel<64, 8> : attn_kv_block_merge_kernel<64, 1>)
+                          : (few ? attn_kv_block_merge_kernel<128, 8> : attn_kv_block_merge_kernel<128, 1>);
+  if (cudaLaunchKernelEx(&cfg, kern, a) != cudaSuccess) {
+    launch_status();
+    return RCX_ERR_CUDA;
+  }
+  return launch_status();
+}
+
+int status_exchange_attn_kv_block_tc(cudaStream_t stream, int* status) { return device_status_exchange(stream, status); }
+
+}  // namespace rcx

@@ -12,6 +12,7 @@ namespace rcx {
 
 static std::atomic<int64_t> g_tc_inject_spins{0};
 void attn_tc_set_inject(int64_t spins) { g_tc_inject_spins.store(spins); }
+int64_t attn_tc_inject() { return g_tc_inject_spins.load(); }
 
 static PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   // looked up once, thread-safely

@@ -1,0 +1,167 @@
+// Work split of the attention over a block-scaled KV cache: which key tiles of
+// which item each CTA takes.  Lengths live on the device, so the split is made
+// there, by the same arithmetic in every CTA.
+//
+// An item is (sequence, row tile, KV head); its rows are (token, query head of
+// the group), row r = token r / G, head r % G.  Its key tiles are the window's
+// tiles and the sink tiles before them.  All items' tiles, in the order
+// sequence, row tile, head, form one line of T tiles; CTA i takes tiles
+// [T i / P, T (i + 1) / P), so that ragged lengths, few rows and many rows all
+// load the P CTAs evenly, and only items that a CTA border cuts need a merge.
+// Heads are the fastest index: CTAs that run side by side on one sequence read
+// the same head's keys.
+#pragma once
+#include "kv_block.cuh"
+
+namespace rcx {
+
+// Key tiles (2^LOGT keys each) that rows of tokens n_lo .. n_hi may see.
+struct KeySpan {
+  int sink_tiles, first, n;         // tile u: u < sink_tiles ? u : first + u - sink_tiles
+  int hi;                           // keys end here
+  __device__ __forceinline__ int tile(int u) const { return u < sink_tiles ? u : first + u - sink_tiles; }
+};
+
+template <int LOGT>
+__device__ __forceinline__ KeySpan key_span(int start, int n_lo, int n_hi, int window, int n_sink) {
+  constexpr int T = 1 << LOGT;
+  KeySpan s;
+  s.hi = start + n_hi + 1;
+  const int lo = window > 0 ? max(0, start + n_lo + 1 - window) : 0;
+  s.first = lo >> LOGT;
+  const int sinks = window > 0 ? min(n_sink, lo) : 0;
+  s.sink_tiles = min((sinks + T - 1) >> LOGT, s.first);
+  s.n = s.sink_tiles + ((s.hi + T - 1) >> LOGT) - s.first;
+  return s;
+}
+
+// Entry e = (sequence, row tile).
+struct Entry {
+  int b, r0, rows;                  // first row of the tile, rows in it (0: nothing to do)
+  int start, n_lo, n_hi;            // cached tokens before the call, tokens of the rows
+  KeySpan span;
+};
+
+template <int LOGT>
+__device__ __forceinline__ Entry entry_of(const KvAttnArgs& a, int e) {
+  Entry t;
+  const int rt = a.n_rt == 1 ? 0 : e % a.n_rt;
+  t.b = a.b0 + (a.n_rt == 1 ? e : e / a.n_rt);
+  const SeqRange s = seq_range(a.start, a.count, t.b, a.N, a.c.cap);
+  t.start = s.start;
+  t.r0 = rt * a.rows_item;
+  t.rows = min(s.n * a.G - t.r0, a.rows_item);
+  if (t.rows <= 0) {
+    t.rows = 0;
+    t.n_lo = t.n_hi = 0;
+    t.span.sink_tiles = t.span.first = t.span.n = t.span.hi = 0;
+    return t;
+  }
+  t.n_lo = t.r0 / a.G;
+  t.n_hi = (t.r0 + t.rows - 1) / a.G;
+  t.span = key_span<LOGT>(s.start, t.n_lo, t.n_hi, a.window, a.n_sink);
+  return t;
+}
+
+// First tile of CTA i.
+__device__ __forceinline__ int range_start(int T, int i, int P) { return (int)((int64_t)T * i / P); }
+// The CTA whose range holds tile x (the last i with range_start(i) <= x).
+__device__ __forceinline__ int range_owner(int T, int x, int P) { return (int)((((int64_t)x + 1) * P - 1) / T); }
+
+// Where a CTA begins: entry e, tile `off` of its Hkv * span.n tiles, and the
+// CTA's range [x0, x1).
+struct PlanStart {
+  int e, off, x0, x1;
+};
+
+// Run by one whole warp; CTA 0 also writes the prefix table for the merge.
+template <int LOGT>
+__device__ __forceinline__ PlanStart plan_start(const KvAttnArgs& a, int cta, int lane) {
+  const int E = a.B * a.n_rt, Hkv = a.c.Hkv;
+  PlanStart p;
+  int carry = 0, incl = 0, mine = 0;
+  for (int e0 = 0; e0 < E; e0 += 32) {
+    const int e = e0 + lane;
+    mine = e < E ? entry_of<LOGT>(a, e).span.n * Hkv : 0;
+    incl = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += y;
+    }
+    if (cta == 0 && e < E) a.prefix[e] = carry + incl - mine;
+    carry += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  const int T = carry;
+  if (cta == 0 && lane == 0) a.prefix[E] = T;
+  p.x0 = range_start(T, cta, a.n_cta);
+  p.x1 = range_start(T, cta + 1, a.n_cta);
+  p.e = 0;
+  p.off = 0;
+  if (p.x0 >= p.x1) return p;
+  carry = 0;
+  for (int e0 = 0; e0 < E; e0 += 32) {
+    if (E > 32) {
+      const int e = e0 + lane;
+      mine = e < E ? entry_of<LOGT>(a, e).span.n * Hkv : 0;
+      incl = mine;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += y;
+      }
+    }
+    const uint32_t past = __ballot_sync(0xffffffffu, carry + incl > p.x0);
+    if (past) {
+      const int l = __ffs(past) - 1;
+      p.e = e0 + l;
+      p.off = p.x0 - (carry + __shfl_sync(0xffffffffu, incl - mine, l));
+      break;
+    }
+    carry += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  return p;
+}
+
+// Walk over the CTA's segments: parts [u0, u1) of one item's tiles.
+struct SegWalk {
+  int e, off, x, x0, x1;
+  Entry t;
+  int hk, u0, u1;
+  bool fresh;                       // t is entry e
+  __device__ __forceinline__ void init(const PlanStart& p) {
+    e = p.e;
+    off = p.off;
+    x = x0 = p.x0;
+    x1 = p.x1;
+    fresh = false;
+  }
+  template <int LOGT>
+  __device__ __forceinline__ bool next(const KvAttnArgs& a) {
+    const int E = a.B * a.n_rt;
+    while (x < x1 && e < E) {
+      if (!fresh) {
+        t = entry_of<LOGT>(a, e);
+        fresh = true;
+      }
+      if (off >= t.span.n * a.c.Hkv) {
+        off -= t.span.n * a.c.Hkv;
+        ++e;
+        fresh = false;
+        continue;
+      }
+      hk = off / t.span.n;
+      u0 = off - hk * t.span.n;
+      u1 = min(t.span.n, u0 + (x1 - x));
+      off += u1 - u0;
+      x += u1 - u0;
+      return true;
+    }
+    return false;
+  }
+  // the segment's place among the CTA's partials: 0 if it opens the range, else 1
+  __device__ __forceinline__ int slot() const { return x - (u1 - u0) == x0 ? 0 : 1; }
+  __device__ __forceinline__ bool whole() const { return u0 == 0 && u1 == t.span.n; }
+};
+
+}  // namespace rcx

@@ -17,6 +17,10 @@ struct RopeArgs;
 struct MergeArgs;
 struct DecodeArgs;
 struct QuantArgs;
+struct RopeAxesArgs;
+struct KvAppendArgs;
+struct KvReadArgs;
+struct KvAttnArgs;
 
 // Counts a launch of `kind` (rcx_kernel_kind); with timing on, records CUDA
 // events around it on `stream`.  Defined in rcx_api.cu.
@@ -47,6 +51,8 @@ inline int allow_smem(K kernel, size_t bytes) {
 // ---- k_rope.cu
 int rope_apply_launch(const RopeArgs& a, int dtype, int grid, int block, cudaStream_t stream);
 
+int rope_axes_launch(const RopeAxesArgs& a, int dtype, dim3 grid, int block, cudaStream_t stream);
+
 // ---- k_merge.cu
 int merge_launch(const MergeArgs& a, int out_dtype, int grid, cudaStream_t stream);
 
@@ -60,6 +66,7 @@ int attn_simt_launch_bf16_bf16(const AttnArgs& a, cudaStream_t stream);
 int attn_tc_launch(const AttnArgs& a, const rcx_tensor& q, const rcx_tensor& k, const rcx_tensor& v,
                    const rcx_tensor& o, cudaStream_t stream);
 void attn_tc_set_inject(int64_t spins);
+int64_t attn_tc_inject();
 
 // ---- k_decode.cu
 int decode_launch(const DecodeArgs& a, int G, bool tensor_core, dim3 grid, cudaStream_t stream);
@@ -69,10 +76,29 @@ int decode_combine_launch(const DecodeArgs& a, int out_dtype, int grid, cudaStre
 // rows16: bf16 rows and code rows both 16-byte aligned (eight-lanes-per-row kernel)
 int quantize_i8_launch(const QuantArgs& a, bool rows16, int grid, cudaStream_t stream);
 
+// ---- k_kv_block.cu, k_attn_kv_block_*.cu (kind: 0 int8, 1 e4m3 codes)
+int kv_block_append_launch(const KvAppendArgs& a, int dtype, int kind, dim3 grid, int block, cudaStream_t stream);
+int kv_block_read_launch(const KvReadArgs& a, int dtype, int kind, dim3 grid, cudaStream_t stream);
+constexpr int kKvFewRows = 32;         // rows (tokens x heads of a group) up to which the mma.sync kernel runs
+constexpr int kKvFewTile = 32;         // its key tile and resident CTAs
+constexpr int kKvFewCtasPerSm = 2;
+constexpr int kKvTcRows = 256;         // rows of an item of the tcgen05 kernel, and its key tile
+constexpr int kKvTcTile = 128;
+constexpr int kKvMaxSlice = 4096;      // sequences a launch takes
+constexpr int kKvReadPerCta = 512;     // 16-code pieces a CTA of the read kernel takes
+int attn_kv_block_launch_int8(const KvAttnArgs& a, cudaStream_t stream);
+int attn_kv_block_launch_e4m3(const KvAttnArgs& a, cudaStream_t stream);
+int attn_kv_block_tc_launch(const KvAttnArgs& a, int kind, cudaStream_t stream);
+int attn_kv_block_merge_launch(const KvAttnArgs& a, cudaStream_t stream);
+
 // Device status words: every translation unit whose kernels have bounded
 // waits keeps its own word; these read one into *status and clear it
 // (stream-ordered, synchronising `stream`).
 int status_exchange_attn_tc(cudaStream_t stream, int* status);
 int status_exchange_rope(cudaStream_t stream, int* status);
+int status_exchange_kv_block(cudaStream_t stream, int* status);
+int status_exchange_attn_kv_block_int8(cudaStream_t stream, int* status);
+int status_exchange_attn_kv_block_e4m3(cudaStream_t stream, int* status);
+int status_exchange_attn_kv_block_tc(cudaStream_t stream, int* status);
 
 }  // namespace rcx

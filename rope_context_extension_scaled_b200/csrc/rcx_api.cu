@@ -20,6 +20,8 @@
 #include "attn_simt.cuh"
 #include "attn_decode.cuh"
 #include "kv_int8.cuh"
+#include "kv_block_args.h"
+#include "rope_axes.cuh"
 #include "rope_freqs.inc"
 
 using namespace rcx;
@@ -104,7 +106,7 @@ constexpr int kAbiVersion = 100;
 
 inline cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s); }
 
-inline int elem_size(int dtype) { return dtype == RCX_BF16 ? 2 : dtype == RCX_I8 ? 1 : 4; }
+inline int elem_size(int dtype) { return dtype == RCX_BF16 ? 2 : dtype == RCX_I8 || dtype == RCX_E4M3 ? 1 : 4; }
 
 int64_t align256(int64_t x) { return (x + 255) & ~int64_t(255); }
 
@@ -226,6 +228,93 @@ int rope_apply_impl(const rcx_tensor& q, const rcx_tensor& k, const rcx_tensor& 
   const int64_t passes = (a.n_tok + tpb - 1) / tpb;
   const int grid = (int)std::min<int64_t>(passes, (int64_t)sm_count() * kRopeCtasPerSm);
   return rope_apply_launch(a, dtype, grid, tpb * a.d_chunks, stream);
+}
+
+// ------------------------------------------------------------------ rope_axes
+
+int rope_axes_map_host(const int64_t* sections, int n_axes, int interleaved, int pairs, int32_t* out) {
+  if (!sections || !out || n_axes < 1 || n_axes > 256 || pairs < 1 || pairs > kMaxPairs) return RCX_ERR_INVALID_ARG;
+  int64_t sum = 0;
+  for (int x = 0; x < n_axes; ++x) {
+    if (sections[x] < 0 || sections[x] > pairs) return RCX_ERR_INVALID_ARG;
+    sum += sections[x];
+  }
+  if (sum != pairs) return RCX_ERR_INVALID_ARG;
+  int i = 0;
+  if (!interleaved) {
+    for (int x = 0; x < n_axes; ++x)
+      for (int64_t j = 0; j < sections[x]; ++j) out[i++] = x;
+  } else {
+    for (int64_t turn = 0; i < pairs; ++turn)
+      for (int x = 0; x < n_axes; ++x)
+        if (sections[x] > turn) out[i++] = x;
+  }
+  return RCX_OK;
+}
+
+int rope_axes_impl(const rcx_tensor& q, const rcx_tensor& k, const rcx_tensor& q_out, const rcx_tensor& k_out,
+                   const int64_t* positions, int n_axes, int64_t stride_axis, int64_t stride_batch,
+                   const double* inv_freq, const int32_t* axis, int flags, cudaStream_t stream) {
+  if (!inv_freq || !axis || n_axes < 1 || n_axes > 256 || stride_axis < 0 || stride_batch < 0)
+    return RCX_ERR_INVALID_ARG;
+  if (flags & ~(RCX_ROPE_HALVES | RCX_ROPE_INVERSE)) return RCX_ERR_INVALID_ARG;
+  const bool has_q = q.ptr != nullptr, has_k = k.ptr != nullptr;
+  if (!has_q && !has_k) return RCX_OK;
+  const rcx_tensor& ref = has_q ? q : k;
+  const int dtype = ref.dtype;
+  const int64_t B = ref.shape[0], N = ref.shape[1], D = ref.shape[3];
+  if (D < 2 || D > 2 * kMaxPairs || (D & 1)) return RCX_ERR_INVALID_ARG;
+  const rcx_tensor* ins[2] = {&q, &k};
+  const rcx_tensor* outs[2] = {&q_out, &k_out};
+  int64_t heads = 0;
+  for (int i = 0; i < 2; ++i) {
+    if (!ins[i]->ptr) continue;
+    int st = check_act(*ins[i]);
+    if (st) return st;
+    st = check_act(*outs[i]);
+    if (st) return st;
+    if (ins[i]->dtype != dtype || outs[i]->dtype != dtype) return RCX_ERR_INVALID_ARG;
+    if (ins[i]->shape[0] != B || ins[i]->shape[1] != N || ins[i]->shape[3] != D) return RCX_ERR_INVALID_ARG;
+    for (int j = 0; j < 4; ++j)
+      if (outs[i]->shape[j] != ins[i]->shape[j]) return RCX_ERR_INVALID_ARG;
+    heads += ins[i]->shape[2];
+  }
+  for (int64_t i = 0; i < D / 2; ++i)
+    if (axis[i] < 0 || axis[i] >= n_axes) return RCX_ERR_INVALID_ARG;
+  const int per_unit = 16 / elem_size(dtype);           // pairs a thread's two vectors hold
+  if (D % (2 * per_unit)) return RCX_ERR_UNSUPPORTED;
+  for (int i = 0; i < 2; ++i)
+    if (ins[i]->ptr && (!vec16_ok(*ins[i]) || !vec16_ok(*outs[i]))) return RCX_ERR_ALIGNMENT;
+  if (B == 0 || N == 0 || heads == 0) return RCX_OK;
+  if (!positions) return RCX_ERR_INVALID_ARG;
+  if (heads > 0x7fffffff) return RCX_ERR_UNSUPPORTED;
+  RopeAxesArgs a;
+  std::memset(&a, 0, sizeof(a));
+  if (has_q) { a.q_in = make_view(q); a.q_out = make_view(q_out); }
+  if (has_k) { a.k_in = make_view(k); a.k_out = make_view(k_out); }
+  a.positions = positions;
+  a.pos_sa = stride_axis;
+  a.pos_sb = stride_batch;
+  a.n_tok = B * N;
+  a.N = N;
+  a.units = (int)(D / 2 / per_unit);
+  a.halves = flags & RCX_ROPE_HALVES ? 1 : 0;
+  a.inverse = flags & RCX_ROPE_INVERSE ? 1 : 0;
+  for (int i = 0; i < (int)(D / 2); ++i) {
+    a.f.theta[i] = inv_freq[i];
+    a.axis[i] = (uint8_t)axis[i];
+  }
+  const int tpb = std::max(1, kRaThreads / a.units);    // units <= 32
+  const int64_t passes = (a.n_tok + tpb - 1) / tpb;
+  // One CTA column takes all heads once the tokens alone fill the GPU; below
+  // that the heads are dealt out, kRaGroup at least to each.
+  const int64_t want = (int64_t)sm_count() * kRaCtasPerSm;
+  const int64_t groups = (heads + kRaGroup - 1) / kRaGroup;
+  const int64_t cols = std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(groups, 65535), want / passes));
+  a.heads_per_y = (int)((groups + cols - 1) / cols) * kRaGroup;
+  const int64_t ny = (heads + a.heads_per_y - 1) / a.heads_per_y;
+  const int64_t nx = std::min<int64_t>(passes, std::max<int64_t>(1, want));
+  return rope_axes_launch(a, dtype, dim3((unsigned)nx, (unsigned)ny), tpb * a.units, stream);
 }
 
 // ---------------------------------------------------------------------- merge
@@ -524,15 +613,217 @@ int decode_i8_impl(const rcx_tensor& q, const rcx_tensor& k, const float* k_scal
   return decode_combine_launch(a, o.dtype, grid2, stream);
 }
 
+// --------------------------------------------------------- block-scaled cache
+
+// Checks the pools, scales and table of a cache and fills the kernels' view.
+int kv_blocks_check(const rcx_kv_blocks* cache, KvBlockView* v, int* kind) {
+  if (!cache) return RCX_ERR_INVALID_ARG;
+  const rcx_kv_blocks& c = *cache;
+  if (c.k.dtype != c.v.dtype) return RCX_ERR_INVALID_ARG;
+  if (c.k.dtype != RCX_I8 && c.k.dtype != RCX_E4M3) return RCX_ERR_INVALID_ARG;
+  for (int i = 0; i < 4; ++i)
+    if (c.k.shape[i] < 1 || c.k.shape[i] != c.v.shape[i]) return RCX_ERR_INVALID_ARG;
+  const rcx_tensor* ts[2] = {&c.k, &c.v};
+  for (const rcx_tensor* t : ts) {
+    if (!t->ptr || t->stride[3] != 1) return RCX_ERR_INVALID_ARG;
+    for (int i = 0; i < 3; ++i)
+      if (t->stride[i] < 0) return RCX_ERR_INVALID_ARG;
+  }
+  if (!c.k_scale || !c.v_scale || c.B < 0 || c.width < 1 || c.table_stride < 0) return RCX_ERR_INVALID_ARG;
+  if (c.B > 0 && !c.table) return RCX_ERR_INVALID_ARG;
+  const int64_t block = c.k.shape[1], D = c.k.shape[3];
+  if (block != 16 && block != 32 && block != 64 && block != 128) return RCX_ERR_UNSUPPORTED;
+  if (D != 64 && D != 128) return RCX_ERR_UNSUPPORTED;
+  // 32-bit token and block numbers, and heads that fit a grid dimension twice
+  if (c.k.shape[0] > 0x7fffffff || c.k.shape[2] > 32767 || c.B > 0x7fffffff) return RCX_ERR_UNSUPPORTED;
+  if (c.width > (0x7fffffff - 1024) / block) return RCX_ERR_UNSUPPORTED;
+  if (!aligned_rows(c.k, 16) || !aligned_rows(c.v, 16)) return RCX_ERR_ALIGNMENT;
+  if (reinterpret_cast<uintptr_t>(c.k_scale) % 4 || reinterpret_cast<uintptr_t>(c.v_scale) % 4 ||
+      reinterpret_cast<uintptr_t>(c.table) % 4)
+    return RCX_ERR_ALIGNMENT;
+  v->k = static_cast<uint8_t*>(c.k.ptr);
+  v->v = static_cast<uint8_t*>(c.v.ptr);
+  v->ks = c.k_scale;
+  v->vs = c.v_scale;
+  v->k_sb = c.k.stride[0]; v->k_sn = c.k.stride[1]; v->k_sh = c.k.stride[2];
+  v->v_sb = c.v.stride[0]; v->v_sn = c.v.stride[1]; v->v_sh = c.v.stride[2];
+  v->table = c.table;
+  v->t_sb = c.table_stride;
+  v->n_blocks = (int)c.k.shape[0];
+  v->block_log2 = block == 16 ? 4 : block == 32 ? 5 : block == 64 ? 6 : 7;
+  v->Hkv = (int)c.k.shape[2];
+  v->cap = (int)(c.width * block);
+  *kind = c.k.dtype == RCX_I8 ? 0 : 1;
+  return RCX_OK;
+}
+
+// K and V rows [B, n, Hkv, d] beside a cache: shapes, one dtype, alignment.
+int kv_rows_check(const rcx_tensor& k, const rcx_tensor& v, const rcx_kv_blocks& c) {
+  int st;
+  if ((st = check_act(k)) || (st = check_act(v))) return st;
+  if (k.dtype != v.dtype) return RCX_ERR_INVALID_ARG;
+  for (int i = 0; i < 4; ++i)
+    if (k.shape[i] != v.shape[i]) return RCX_ERR_INVALID_ARG;
+  if (k.shape[0] != c.B || k.shape[2] != c.k.shape[2] || k.shape[3] != c.k.shape[3]) return RCX_ERR_INVALID_ARG;
+  if (!aligned_rows(k, 16) || !aligned_rows(v, 16)) return RCX_ERR_ALIGNMENT;
+  return RCX_OK;
+}
+
+int kv_append_impl(const rcx_tensor& k, const rcx_tensor& v, const rcx_kv_blocks* cache, const int64_t* start,
+                   const int64_t* count, cudaStream_t stream) {
+  KvAppendArgs a;
+  std::memset(&a, 0, sizeof(a));
+  int st, kind = 0;
+  if ((st = kv_blocks_check(cache, &a.c, &kind)) || (st = kv_rows_check(k, v, *cache))) return st;
+  const int64_t B = cache->B, N = k.shape[1], D = k.shape[3], block = cache->k.shape[1];
+  if (B == 0 || N == 0) return RCX_OK;
+  if (!start) return RCX_ERR_INVALID_ARG;
+  if (N > a.c.cap) return RCX_ERR_INVALID_ARG;           // more tokens than a table row holds
+  a.k = make_view(k);
+  a.v = make_view(v);
+  a.start = start;
+  a.count = count;
+  a.N = (int)N;
+  a.d_log2 = D == 64 ? 6 : 7;
+  const unsigned nb = (unsigned)((N + block - 2) / block + 1);      // blocks N tokens may touch
+  for (int64_t b0 = 0; b0 < B; b0 += 65535) {
+    a.b0 = (int)b0;
+    dim3 grid(nb, (unsigned)(2 * a.c.Hkv), (unsigned)std::min<int64_t>(B - b0, 65535));
+    if ((st = kv_block_append_launch(a, k.dtype, kind, grid, (int)(block * D / 32), stream))) return st;
+  }
+  return RCX_OK;
+}
+
+int kv_read_impl(const rcx_kv_blocks* cache, const int64_t* len, const rcx_tensor& k, const rcx_tensor& v,
+                 cudaStream_t stream) {
+  KvReadArgs a;
+  std::memset(&a, 0, sizeof(a));
+  int st, kind = 0;
+  if ((st = kv_blocks_check(cache, &a.c, &kind)) || (st = kv_rows_check(k, v, *cache))) return st;
+  const int64_t B = cache->B, n = k.shape[1], D = k.shape[3];
+  if (B == 0 || n == 0) return RCX_OK;
+  if (!len) return RCX_ERR_INVALID_ARG;
+  const int64_t pieces = n * a.c.Hkv * (D / 16);
+  if (n > 0x7fffffff || pieces > 0x7fffffff) return RCX_ERR_UNSUPPORTED;
+  a.k = make_view(k);
+  a.v = make_view(v);
+  a.len = len;
+  a.n = (int)n;
+  a.d_log2 = D == 64 ? 6 : 7;
+  for (int64_t b0 = 0; b0 < B; b0 += 65535) {
+    a.b0 = (int)b0;
+    dim3 grid((unsigned)((pieces + kKvReadPerCta - 1) / kKvReadPerCta), (unsigned)std::min<int64_t>(B - b0, 65535));
+    if ((st = kv_block_read_launch(a, k.dtype, kind, grid, stream))) return st;
+  }
+  return RCX_OK;
+}
+
+// Which kernel runs, how many sequences a launch takes, and the workspace.
+struct KvAttnPlan {
+  bool few;
+  int rows_item, n_rt, n_cta;
+  int64_t slice, off_lse, off_prefix, total;
+};
+
+int kv_attn_plan(const rcx_tensor& q, const KvBlockView& c, int64_t B, KvAttnPlan* p) {
+  const int64_t N = q.shape[1], Hq = q.shape[2], D = q.shape[3];
+  if (Hq < 1 || Hq % c.Hkv || D < 1) return RCX_ERR_INVALID_ARG;
+  const int64_t G = Hq / c.Hkv;
+  if (G > 65535 || N > 0x3fffffff / G) return RCX_ERR_UNSUPPORTED;
+  const int64_t rows = N * G;
+  p->few = rows <= kKvFewRows;
+  p->rows_item = p->few ? (int)((rows + 7) / 8 * 8) : kKvTcRows;
+  p->n_rt = p->few ? 1 : (int)((rows + kKvTcRows - 1) / kKvTcRows);
+  const int64_t tile = p->few ? kKvFewTile : kKvTcTile;
+  // key tiles of one sequence: all its items', sinks' partial tile included
+  const int64_t tiles = (int64_t)c.Hkv * p->n_rt * (((int64_t)c.cap + tile - 1) / tile + 1);
+  if (tiles > 0x7fffffff) return RCX_ERR_UNSUPPORTED;    // the kernels count tiles in 32 bits
+  p->slice = std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(B, kKvMaxSlice), 0x7fffffff / tiles));
+  const int64_t ctas = (int64_t)sm_count() * (p->few ? kKvFewCtasPerSm : 1);
+  p->n_cta = (int)std::min<int64_t>(ctas, p->slice * tiles);
+  p->off_lse = align256((int64_t)p->n_cta * 2 * p->rows_item * D * 4);
+  p->off_prefix = align256(p->off_lse + (int64_t)p->n_cta * 2 * p->rows_item * 4);
+  p->total = align256(p->off_prefix + (p->slice * p->n_rt + 1) * 4);
+  return RCX_OK;
+}
+
+int kv_attn_impl(const rcx_tensor& q, const rcx_kv_blocks* cache, const int64_t* start, const int64_t* count,
+                 const rcx_tensor& o, const rcx_tensor& lse, int64_t window, int64_t n_sink, double temperature,
+                 void* workspace, int64_t workspace_bytes, cudaStream_t stream) {
+  KvAttnArgs a;
+  std::memset(&a, 0, sizeof(a));
+  int st, kind = 0;
+  if ((st = kv_blocks_check(cache, &a.c, &kind)) || (st = check_act(q)) || (st = check_act(o))) return st;
+  const int64_t B = q.shape[0], N = q.shape[1], Hq = q.shape[2], D = q.shape[3];
+  if (B != cache->B || D != cache->k.shape[3]) return RCX_ERR_INVALID_ARG;
+  for (int i = 0; i < 4; ++i)
+    if (o.shape[i] != q.shape[i]) return RCX_ERR_INVALID_ARG;
+  if (lse.ptr && (st = check_lse(lse, B, Hq, N))) return st;
+  if (window < 0 || n_sink < 0) return RCX_ERR_INVALID_ARG;
+  if (!(temperature > 0.0) || !std::isfinite(temperature)) return RCX_ERR_INVALID_ARG;
+  KvAttnPlan p;
+  if ((st = kv_attn_plan(q, a.c, B, &p))) return st;
+  if (q.dtype != RCX_BF16) return RCX_ERR_UNSUPPORTED;
+  if (!aligned_rows(q, 16) || !aligned_rows(o, o.dtype == RCX_BF16 ? 8 : 16)) return RCX_ERR_ALIGNMENT;
+  if (B == 0 || N == 0) return RCX_OK;
+  if (N > a.c.cap) return RCX_ERR_INVALID_ARG;           // rows that no token of the cache can be
+  if (!start) return RCX_ERR_INVALID_ARG;
+  if (!workspace || workspace_bytes < p.total) return RCX_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(workspace) % 256) return RCX_ERR_ALIGNMENT;
+  a.q = make_view(q);
+  a.o = make_view(o);
+  a.o_bf16 = o.dtype == RCX_BF16;
+  a.lse = static_cast<float*>(lse.ptr);
+  a.lse_sb = lse.ptr ? lse.stride[0] : 0;
+  a.lse_sh = lse.ptr ? lse.stride[1] : 0;
+  a.start = start;
+  a.count = count;
+  a.N = (int)N;
+  a.G = (int)(Hq / a.c.Hkv);
+  a.window = (int)std::min<int64_t>(window, 0x7fffffff);
+  a.n_sink = (int)std::min<int64_t>(n_sink, a.c.cap);
+  a.scale_log2 = (float)(1.4426950408889634074 / (std::sqrt((double)D) * temperature));
+  a.rows_item = p.rows_item;
+  a.n_rt = p.n_rt;
+  a.n_cta = p.n_cta;
+  char* ws = static_cast<char*>(workspace);
+  a.part_o = reinterpret_cast<float*>(ws);
+  a.part_lse = reinterpret_cast<float*>(ws + p.off_lse);
+  a.prefix = reinterpret_cast<int*>(ws + p.off_prefix);
+  a.inject_spins = p.few ? 0 : attn_tc_inject();
+  for (int64_t b0 = 0; b0 < B; b0 += p.slice) {
+    a.b0 = (int)b0;
+    a.B = (int)std::min<int64_t>(B - b0, p.slice);
+    st = !p.few ? attn_kv_block_tc_launch(a, kind, stream)
+         : kind == 0 ? attn_kv_block_launch_int8(a, stream) : attn_kv_block_launch_e4m3(a, stream);
+    if (st) return st;
+    if ((st = attn_kv_block_merge_launch(a, stream))) return st;
+  }
+  return RCX_OK;
+}
+
 // -------------------------------------------------------------- device status
 
-// Reads and clears the status words of every kernel family with bounded
-// waits (synchronising `s`); the tensor-core attention's word wins if both are set.
-int device_status_all(cudaStream_t s, int* out) {
+// Reads and clears the status words of the kernels that the ring forward runs
+// (synchronising `s`); the tensor-core attention's word wins if both are set.
+int device_status_ring(cudaStream_t s, int* out) {
   int a = 0, b = 0, st;
   if ((st = status_exchange_attn_tc(s, &a))) return st;
   if ((st = status_exchange_rope(s, &b))) return st;
   *out = a != 0 ? a : b;
+  return RCX_OK;
+}
+
+// The same of every kernel family that records a status.
+int device_status_all(cudaStream_t s, int* out) {
+  int st, x = 0;
+  if ((st = device_status_ring(s, out))) return st;
+  int (*const words[])(cudaStream_t, int*) = {status_exchange_attn_kv_block_tc, status_exchange_attn_kv_block_int8,
+                                              status_exchange_attn_kv_block_e4m3, status_exchange_kv_block};
+  for (auto word : words) {
+    if ((st = word(s, &x))) return st;
+    if (*out == RCX_OK) *out = x;
+  }
   return RCX_OK;
 }
 
@@ -738,6 +1029,7 @@ const char* rcx_status_string(int status) {
     case RCX_ERR_ALIGNMENT: return "misaligned pointer or stride";
     case RCX_ERR_CUDA: return "CUDA error";
     case RCX_ERR_DEVICE_TIMEOUT: return "device-side wait timed out";
+    case RCX_ERR_DEVICE_INDEX: return "length or block number out of range on the device";
     default: return "unknown status";
   }
 }
@@ -754,6 +1046,44 @@ int rcx_rope_freqs_per_pair(double base, int d, const double* factors, double* i
 int rcx_rope_apply(rcx_tensor q, rcx_tensor k, rcx_tensor q_out, rcx_tensor k_out, const int64_t* positions,
                    int64_t n_positions, const double* inv_freq, void* stream) {
   return rope_apply_impl(q, k, q_out, k_out, positions, n_positions, inv_freq, as_stream(stream));
+}
+
+int rcx_rope_axes_map(const int64_t* sections, int n_axes, int interleaved, int pairs, int32_t* axis_out) {
+  return rope_axes_map_host(sections, n_axes, interleaved, pairs, axis_out);
+}
+
+int rcx_rope_axes_apply(rcx_tensor q, rcx_tensor k, rcx_tensor q_out, rcx_tensor k_out, const int64_t* positions,
+                        int n_axes, int64_t stride_axis, int64_t stride_batch, const double* inv_freq,
+                        const int32_t* axis, int flags, void* stream) {
+  return rope_axes_impl(q, k, q_out, k_out, positions, n_axes, stride_axis, stride_batch, inv_freq, axis, flags,
+                        as_stream(stream));
+}
+
+int rcx_kv_block_append(rcx_tensor k, rcx_tensor v, const rcx_kv_blocks* cache, const int64_t* start,
+                        const int64_t* count, void* stream) {
+  return kv_append_impl(k, v, cache, start, count, as_stream(stream));
+}
+
+int rcx_kv_block_read(const rcx_kv_blocks* cache, const int64_t* len, rcx_tensor k_out, rcx_tensor v_out,
+                      void* stream) {
+  return kv_read_impl(cache, len, k_out, v_out, as_stream(stream));
+}
+
+int64_t rcx_attn_kv_block_workspace_size(rcx_tensor q, const rcx_kv_blocks* cache) {
+  KvBlockView v;
+  KvAttnPlan p;
+  int kind;
+  if (check_act(q) || kv_blocks_check(cache, &v, &kind) || q.shape[0] != cache->B ||
+      q.shape[3] != cache->k.shape[3] || kv_attn_plan(q, v, cache->B, &p))
+    return -1;
+  return p.total;
+}
+
+int rcx_attn_kv_block_fwd(rcx_tensor q, const rcx_kv_blocks* cache, const int64_t* start, const int64_t* count,
+                          rcx_tensor o, rcx_tensor lse, int64_t window, int64_t n_sink, double temperature,
+                          void* workspace, int64_t workspace_bytes, void* stream) {
+  return kv_attn_impl(q, cache, start, count, o, lse, window, n_sink, temperature, workspace, workspace_bytes,
+                      as_stream(stream));
 }
 
 int rcx_attn_blockwise_fwd(rcx_tensor q, rcx_tensor k, rcx_tensor v, rcx_tensor o, rcx_tensor lse,
@@ -944,7 +1274,7 @@ int rcx_ring_attn_fwd_host(rcx_tensor q, rcx_tensor k, rcx_tensor v, rcx_tensor 
   // kernels is reported here (and the status word cleared), not left for a
   // later rcx_device_status().
   int dev_st = RCX_OK;
-  if (st == RCX_OK && device_status_all(s, &dev_st) != RCX_OK) st = RCX_ERR_CUDA;
+  if (st == RCX_OK && device_status_ring(s, &dev_st) != RCX_OK) st = RCX_ERR_CUDA;
   if (st == RCX_OK && dev_st != RCX_OK) st = dev_st;
   return st;
 }
