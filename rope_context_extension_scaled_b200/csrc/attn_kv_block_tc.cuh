@@ -11,14 +11,14 @@
 // heads fills the MMA's 128 rows at any group size.  512 threads:
 //   warps 0-3   softmax, Q load and epilogue of slot 0 (a thread per row)
 //   warps 4-7   the same of slot 1 (idle when an item has at most 128 rows)
-//   warps 8-11  converters: codes of the next tile come into registers while
-//               the current one is turned into fp16 and stored as
-//               128B-swizzled K and V tiles (two stages), so the cache is read
-//               as it is stored, through its table, and no copy of it is made
+//   warps 8-11  converters: codes of the next tile are copied to shared memory
+//               (cp.async) while the current one is turned into fp16 and stored
+//               as 128B-swizzled K and V tiles (two stages), so the cache is
+//               read as it is stored, through its table, and never copied whole
 //   warp  12    MMA issuer and TMEM owner (13-15 have nothing to do)
-// The softmax threads hold half a row of S beside packed weights: registers move
-// to them from the other warpgroups (setmaxnreg; 184, 96 and 40 a thread add up
-// to 64,512 of the launch's 65,536).
+// The softmax threads hold a row of S: registers move to them from the other
+// warpgroups (setmaxnreg; 2 x 200, 72 and 40 a thread are the launch's 65,536),
+// and each warp's place in the walk over segments is kept in shared memory.
 // TMEM: S0 | S1 | O0 | O1, 128 columns each.  P overwrites the first half of its
 // S; O += P V takes P from TMEM.
 //  * d order: a word's codes leave codes4_to_h2 in the order 0, 2, 1, 3.  Q is
@@ -43,7 +43,7 @@ constexpr int kBtN = kKvTcTile;                 // keys per tile
 constexpr int kBtLogN = 7;
 static_assert(1 << kBtLogN == kBtN && 2 * kBtM == kKvTcRows, "tile");
 constexpr int kBtThreads = 512;
-constexpr int kBtRegsSoftmax = 184, kBtRegsConv = 96, kBtRegsMma = 40;
+constexpr int kBtRegsSoftmax = 200, kBtRegsConv = 72, kBtRegsMma = 40;
 static_assert(128 * (2 * kBtRegsSoftmax + kBtRegsConv + kBtRegsMma) <= 512 * 128, "registers of the launch");
 constexpr int kBtConv = 8;                      // first converter warp
 constexpr int kBtMma = 12;
@@ -64,15 +64,45 @@ struct BtMeta {
   uint32_t pad;
 };
 
+// A warp's place in the walk (e, off, x: see SegWalk) and its current segment.
+struct BtSeg {
+  int e, off, x, x0, x1;
+  int ok;                                       // a segment is there
+  int b, hk, r0, rows, start;
+  KeySpan span;
+  int u0, n, slot, whole;
+};
+
+// Next segment of the calling warp: one lane walks, all read.
+__device__ __forceinline__ bool bt_next(BtSeg* g, const KvAttnArgs& a, int lane) {
+  __syncwarp();                                 // the old segment has been read
+  if (lane == 0) {
+    SegWalk w;
+    w.e = g->e; w.off = g->off; w.x = g->x; w.x0 = g->x0; w.x1 = g->x1;
+    w.fresh = false;
+    g->ok = w.next<kBtLogN>(a);
+    if (g->ok) {
+      g->e = w.e; g->off = w.off; g->x = w.x;
+      g->b = w.t.b; g->hk = w.hk; g->r0 = w.t.r0; g->rows = w.t.rows; g->start = w.t.start;
+      g->span = w.t.span;
+      g->u0 = w.u0; g->n = w.u1 - w.u0; g->slot = w.slot(); g->whole = w.whole();
+    }
+  }
+  __syncwarp();
+  return g->ok;
+}
+
 template <int D>
 struct BtSmem {
   static constexpr uint32_t tile = kBtHalf * (D / 64);
   static constexpr uint32_t q = 0;
   static constexpr uint32_t k = q + 2 * tile;
   static constexpr uint32_t v = k + kBtStages * tile;
-  static constexpr uint32_t bar = v + kBtStages * tile;
+  static constexpr uint32_t raw = v + kBtStages * tile;            // codes of the next K and V tile
+  static constexpr uint32_t bar = raw + 2 * kBtN * D;
   static constexpr uint32_t meta = bar + 256;
-  static constexpr uint32_t total = meta + kBtMeta * sizeof(BtMeta) + 64 + 1024;   // + plan, alignment slack
+  static constexpr uint32_t seg = meta + kBtMeta * sizeof(BtMeta);
+  static constexpr uint32_t total = seg + 13 * sizeof(BtSeg) + 1024;   // + alignment slack
 };
 
 // kind::f16 descriptor: fp16 A and B, fp32 accumulator, M = 128
@@ -80,13 +110,19 @@ __host__ __device__ constexpr uint32_t idesc_f16(bool b_mn_major, int n) {
   return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kBtM >> 4) << 24);
 }
 
-// (a, b) * f + c, the product rounded before the sum: the row maximum was rounded
-// the same way, so the winner's exponent is c + max exactly, however large the
-// logits.  (An unrounded product may pass the rounded maximum by half a step,
-// which from 2^25 on is more than fp16 weights hold.)
-__device__ __forceinline__ void mul_add2(float& r0, float& r1, float a, float b, float f, float c) {
-  r0 = __fadd_rn(__fmul_rn(a, f), c);
-  r1 = __fadd_rn(__fmul_rn(b, f), c);
+// Packed fp32 arithmetic: two values an instruction.
+// (volatile: the first use of values from tcgen05.ld must stay behind its wait)
+__device__ __forceinline__ void mul2(float& a, float& b, float f) {
+  asm volatile("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %2};\n\t"
+      "mul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "+f"(a), "+f"(b)
+      : "f"(f));
+}
+__device__ __forceinline__ void add2(float& a, float& b, float c, float d) {
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\t"
+      "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "+f"(a), "+f"(b)
+      : "f"(c), "f"(d));
 }
 
 template <int R>
@@ -121,7 +157,7 @@ __global__ void __launch_bounds__(kBtThreads, 1) attn_kv_block_tc_kernel(const _
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::bar + 8 * B_COUNT);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::bar + 8 * B_COUNT + 8);
   BtMeta* meta = reinterpret_cast<BtMeta*>(smem + L::meta);
-  PlanStart* plan = reinterpret_cast<PlanStart*>(smem + L::meta + kBtMeta * sizeof(BtMeta));
+  BtSeg* segs_all = reinterpret_cast<BtSeg*>(smem + L::seg);
 
   const int warp = threadIdx.x / 32;
   const int lane = threadIdx.x % 32;
@@ -140,7 +176,10 @@ __global__ void __launch_bounds__(kBtThreads, 1) attn_kv_block_tc_kernel(const _
   }
   if (warp == 0) {
     const PlanStart p = plan_start<kBtLogN>(a, blockIdx.x, lane);
-    if (lane == 0) *plan = p;
+    if (lane < 13) {
+      BtSeg* g = segs_all + lane;
+      g->e = p.e; g->off = p.off; g->x = g->x0 = p.x0; g->x1 = p.x1;
+    }
   }
   if (warp == kBtMma) tmem_alloc(smem_addr(tmem_slot), 512);
   tc_fence_before();
@@ -151,8 +190,7 @@ __global__ void __launch_bounds__(kBtThreads, 1) attn_kv_block_tc_kernel(const _
   auto tS = [&](int s) { return tmem + 128u * (uint32_t)s; };
   auto tO = [&](int s) { return tmem + 256u + 128u * (uint32_t)s; };
   auto warp_wait = [&](int b, uint32_t par) { return __all_sync(0xffffffffu, mbar_wait(BAR(b), par, abort_flag)); };
-  SegWalk w;
-  w.init(*plan);
+  BtSeg* const w = segs_all + min(warp, 12);
   bool ok = true;
 
   if (warp >= kBtMma) {
@@ -192,9 +230,9 @@ __global__ void __launch_bounds__(kBtThreads, 1) attn_kv_block_tc_kernel(const _
       ok = __shfl_sync(0xffffffffu, got ? 1 : 0, 0) != 0;
     }
     int jg = 0, js[2] = {0, 0}, segs[2] = {0, 0};   // tiles so far (all, per slot), segments per slot
-    while (ok && w.next<kBtLogN>(a)) {
-      const int n = w.u1 - w.u0;
-      const int ns = w.t.rows > kBtM ? 2 : 1;
+    while (ok && bt_next(w, a, lane)) {
+      const int n = w->n;
+      const int ns = w->rows > kBtM ? 2 : 1;
       for (int s = 0; s < ns && ok; ++s) ok = warp_wait(B_QREADY + s, segs[s] & 1);
       if (!ok) break;
       {
@@ -251,21 +289,19 @@ __global__ void __launch_bounds__(kBtThreads, 1) attn_kv_block_tc_kernel(const _
     // a piece of 16 codes becomes two 16-byte chunks of one swizzled 128-byte row;
     // pieces of the upper half store theirs in the other order (bank conflicts)
     const int flip = (pc >> 2) & 1;
-    uint4 kr[kPieces], vr[kPieces];
+    // a thread copies and converts the same pieces, so no barrier stands between
+    const uint4* raw_k = reinterpret_cast<const uint4*>(smem + L::raw) + tid;
+    const uint4* raw_v = raw_k + kPieces * 128;
     int jg = 0;
-    float vref = 0.f;
-    while (ok && w.next<kBtLogN>(a)) {
-      const KeySpan span = w.t.span;
-      const int hi = span.hi;
-      const int32_t* trow = kv.table + (int64_t)w.t.b * kv.t_sb;
-      const uint8_t* kb = kv.k + w.hk * kv.k_sh + pc * 16;
-      const uint8_t* vb = kv.v + w.hk * kv.v_sh + pc * 16;
+    while (ok && bt_next(w, a, lane)) {
+      const int32_t* trow = kv.table + (int64_t)w->b * kv.t_sb;
+      const int u1 = w->u0 + w->n;
       // lane i < 8: block of 16-key group i of tile u (0 behind the keys)
       auto load_phys = [&](int u) {
         int e = 0;
-        if (u < w.u1) {
-          const int key = (span.tile(u) << kBtLogN) + 16 * (lane & 7);
-          if (key < hi) {
+        if (u < u1) {
+          const int key = (w->span.tile(u) << kBtLogN) + 16 * (lane & 7);
+          if (key < w->span.hi) {
             e = trow[key >> lb];
             if ((unsigned)e >= (unsigned)kv.n_blocks) {
               record_device_error(RCX_ERR_DEVICE_INDEX);
@@ -278,26 +314,33 @@ __global__ void __launch_bounds__(kBtThreads, 1) attn_kv_block_tc_kernel(const _
       // lanes 0-7 K, 8-15 V scale of the groups of tile u with blocks ph
       auto load_scale = [&](int u, int ph) {
         float s = 0.f;
-        if (u < w.u1 && lane < 16 && (span.tile(u) << kBtLogN) + 16 * (lane & 7) < hi)
-          s = (lane < 8 ? kv.ks : kv.vs)[(int64_t)ph * kv.Hkv + w.hk];
+        if (u < u1 && lane < 16 && (w->span.tile(u) << kBtLogN) + 16 * (lane & 7) < w->span.hi)
+          s = (lane < 8 ? kv.ks : kv.vs)[(int64_t)ph * kv.Hkv + w->hk];
         return s;
       };
-      auto load_codes = [&](int u, int ph, const uint8_t* base, int64_t sb, int64_t sn, uint4* r) {
-        const int key0 = span.tile(u) << kBtLogN;
+      // codes of tile u -> the thread's raw pieces (keys behind the sequence: zeros, nothing read)
+      auto load_codes = [&](int u, int ph, const uint8_t* base, int64_t sb, int64_t sn, const uint4* raw) {
+        if (u < u1) {
+          const int key0 = w->span.tile(u) << kBtLogN;
+          const uint32_t dst = smem_addr(raw);
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-          const int row = i * kRows + pr;
-          const int phys = __shfl_sync(0xffffffffu, ph, row >> 4);
-          r[i] = make_uint4(0u, 0u, 0u, 0u);      // keys behind the sequence: zeros, nothing read
-          if (key0 + row < hi)
-            r[i] = __ldg(reinterpret_cast<const uint4*>(base + phys * sb + ((key0 + row) & bmask) * sn));
+          for (int i = 0; i < kPieces; ++i) {
+            const int row = i * kRows + pr;
+            const int phys = __shfl_sync(0xffffffffu, ph, row >> 4);
+            const int bytes = key0 + row < w->span.hi ? 16 : 0;
+            const uint8_t* src = base + pc * 16 + (bytes ? phys * sb + ((key0 + row) & bmask) * sn : 0);
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + i * 2048), "l"(src), "r"(bytes)
+                         : "memory");
+          }
         }
+        asm volatile("cp.async.commit_group;" ::: "memory");
       };
-      auto store_tile = [&](uint32_t tile_off, const uint4* r, uint32_t ratios, auto scaled) {
+      auto store_tile = [&](uint32_t tile_off, const uint4* raw, uint32_t ratios, auto scaled) {
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
           const int row = i * kRows + pr;
-          const uint32_t wv[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
+          const uint4 x = raw[i * 128];
+          const uint32_t wv[4] = {x.x, x.y, x.z, x.w};
           uint32_t h[8];
 #pragma unroll
           for (int e = 0; e < 4; ++e) codes4_to_h2<KIND>(wv[e], h[2 * e], h[2 * e + 1]);
@@ -306,8 +349,8 @@ __global__ void __launch_bounds__(kBtThreads, 1) attn_kv_block_tc_kernel(const _
             const __half2 rh = *reinterpret_cast<const __half2*>(&rb);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              const __half2 x = __hmul2(*reinterpret_cast<const __half2*>(&h[e]), rh);
-              h[e] = *reinterpret_cast<const uint32_t*>(&x);
+              const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&h[e]), rh);
+              h[e] = *reinterpret_cast<const uint32_t*>(&y);
             }
           }
           uint8_t* dst = smem + tile_off + (pc >> 2) * kBtHalf + row * 128;
@@ -317,12 +360,19 @@ __global__ void __launch_bounds__(kBtThreads, 1) attn_kv_block_tc_kernel(const _
           *reinterpret_cast<uint4*>(dst + (c0 ^ 1) * 16) = flip ? lo : hi4;
         }
       };
-      int ph = load_phys(w.u0), ph_next = load_phys(w.u0 + 1);
-      float sc = load_scale(w.u0, ph);
-      load_codes(w.u0, ph, kb, kv.k_sb, kv.k_sn, kr);
-      load_codes(w.u0, ph, vb, kv.v_sb, kv.v_sn, vr);
-      vref = 0.f;
-      for (int u = w.u0; u < w.u1; ++u, ++jg) {
+      const uint8_t* kb = kv.k + w->hk * kv.k_sh;
+      const uint8_t* vb = kv.v + w->hk * kv.v_sh;
+      const int u0 = w->u0;
+      int ph_next = load_phys(u0 + 1);
+      float sc;
+      {
+        const int ph = load_phys(u0);
+        sc = load_scale(u0, ph);
+        load_codes(u0, ph, kb, kv.k_sb, kv.k_sn, raw_k);
+        load_codes(u0, ph, vb, kv.v_sb, kv.v_sn, raw_v);
+      }
+      float vref = 0.f;
+      for (int u = u0; u < u1; ++u, ++jg) {
         const int st = jg % kBtStages;
         const uint32_t par = ((jg / kBtStages) & 1) ^ 1;
         const int ph_next2 = load_phys(u + 2);
@@ -338,8 +388,9 @@ __global__ void __launch_bounds__(kBtThreads, 1) attn_kv_block_tc_kernel(const _
         vref = vnew;
         const float ratio = vref > 0.f ? sv / vref * kBtVUp<KIND> : 0.f;
         const uint32_t ratios = f2_to_h2(ratio, ratio);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");   // K's codes
         if (!(ok = warp_wait(B_KEMPTY + st, par))) break;
-        store_tile(L::k + st * L::tile, kr, 0u, std::false_type{});
+        store_tile(L::k + st * L::tile, raw_k, 0u, std::false_type{});
         if (warp == kBtConv) {                    // the tile's scales
           BtMeta* mt = meta + jg % kBtMeta;
           if (lane < 8) mt->ks[lane] = sc;
@@ -352,17 +403,18 @@ __global__ void __launch_bounds__(kBtThreads, 1) attn_kv_block_tc_kernel(const _
         }
         fence_proxy_async_smem();
         mbar_arrive(BAR(B_KFULL + st));
-        if (u + 1 < w.u1) load_codes(u + 1, ph_next, kb, kv.k_sb, kv.k_sn, kr);
+        load_codes(u + 1, ph_next, kb, kv.k_sb, kv.k_sn, raw_k);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");   // V's codes
         if (!(ok = warp_wait(B_VEMPTY + st, par))) break;
-        store_tile(L::v + st * L::tile, vr, ratios, std::true_type{});
+        store_tile(L::v + st * L::tile, raw_v, ratios, std::true_type{});
         fence_proxy_async_smem();
         mbar_arrive(BAR(B_VFULL + st));
-        if (u + 1 < w.u1) load_codes(u + 1, ph_next, vb, kv.v_sb, kv.v_sn, vr);
-        ph = ph_next;
+        load_codes(u + 1, ph_next, vb, kv.v_sb, kv.v_sn, raw_v);
         ph_next = ph_next2;
         sc = sc_next;
       }
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
   } else {
     // ================================================================ softmax + epilogue
     regs_up<kBtRegsSoftmax>();
@@ -371,24 +423,21 @@ __global__ void __launch_bounds__(kBtThreads, 1) attn_kv_block_tc_kernel(const _
     const int r = q4 * 32 + lane;               // row within the slot
     const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
     int jg = 0, js = 0, segs = 0;
-    while (ok && w.next<kBtLogN>(a)) {
-      const int n = w.u1 - w.u0;
-      const int ns = w.t.rows > kBtM ? 2 : 1;
-      if (s >= ns) {
+    while (ok && bt_next(w, a, lane)) {
+      const int n = w->n;
+      if (s * kBtM >= w->rows) {
         jg += n;
         continue;
       }
-      const Entry& t = w.t;
-      const int64_t b = t.b;
-      const bool row_ok = s * kBtM + r < t.rows;
-      const int rr = t.r0 + min(s * kBtM + r, t.rows - 1);     // rows behind the last repeat it
-      const int tok = rr / a.G, hq = w.hk * a.G + rr - tok * a.G;
-      const int gi = t.start + tok;
+      const bool row_ok = s * kBtM + r < w->rows;
+      const int rr = w->r0 + min(s * kBtM + r, w->rows - 1);   // rows behind the last repeat it
+      const int tok = rr / a.G, hq = w->hk * a.G + rr - tok * a.G;
+      const int gi = w->start + tok;
       // ---- Q row -> power-of-two scaled fp16 in shared memory.  The buffer is free:
       // the slot's last OFINAL came after every S MMA that read it.
       float fac;
       {
-        const uint4* qp = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q.ptr) + b * a.q.sb +
+        const uint4* qp = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q.ptr) + (int64_t)w->b * a.q.sb +
                                                          (int64_t)tok * a.q.sn + (int64_t)hq * a.q.sh);
         uint4 x[D / 8];
         uint32_t mx = 0;
@@ -414,11 +463,11 @@ __global__ void __launch_bounds__(kBtThreads, 1) attn_kv_block_tc_kernel(const _
         fence_proxy_async_smem();
         mbar_arrive(BAR(B_QREADY + s));
       }
-      const int ti_lo = t.start + (t.r0 + s * kBtM) / a.G;
-      const int ti_hi = t.start + (t.r0 + min((s + 1) * kBtM, t.rows) - 1) / a.G;
+      // tiles of keys full_lo < key0 <= full_hi, and sink tiles, need no mask for the slot's rows
+      const int full_hi = w->start + (w->r0 + s * kBtM) / a.G + 1 - kBtN;
+      const int full_lo = a.window == 0 ? -1 : w->start + (w->r0 + min((s + 1) * kBtM, w->rows) - 1) / a.G - a.window;
       float m_used = -INFINITY, l = 0.f, vref = 0.f, poison = 0.f;
       for (int j = 0; j < n; ++j) {
-        const int key0 = w.t.span.tile(w.u0 + j) << kBtLogN;
         const int g = jg + j;
         // S first: its phases are counted per slot, and once tile g's S is there the
         // ring's barrier stands at tile g (a slot that sat out segments would take an
@@ -427,91 +476,73 @@ __global__ void __launch_bounds__(kBtThreads, 1) attn_kv_block_tc_kernel(const _
                                                mbar_wait(BAR(B_META + g % kBtMeta), (g / kBtMeta) & 1, abort_flag))))
           break;
         tc_fence_after();
+        float x[128];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tmem_ld32(tS(s) + lane_off + 32 * i, reinterpret_cast<uint32_t*>(x) + 32 * i);
         const BtMeta* mt = meta + g % kBtMeta;
-        const bool full = key0 + kBtN <= ti_lo + 1 &&
-                          (a.window == 0 || key0 > ti_hi - a.window || key0 + kBtN <= a.n_sink);
-        auto clip = [](int x) { return x < -1 ? -1 : (x > kBtN ? kBtN : x); };
-        const int lim = clip(gi - key0);
-        const int win_lo = a.window > 0 ? clip(gi - a.window - key0) : -1;
-        const int snk = a.window > 0 ? clip(a.n_sink - 1 - key0) : -1;
-        const float vfac = mt->vfac;
-        vref = mt->vref;
-        if (const uint32_t vbad = mt->vbad) {   // NaN for the rows that see a marked key
-          for (int c = 0; c < kBtN; ++c)
-            if ((vbad >> (c >> 4)) & 1)
-              if (c <= lim && (c > win_lo || c <= snk)) poison = __uint_as_float(0x7fffffffu);
+        const int key0 = w->span.tile(w->u0 + j) << kBtLogN;
+        const bool full = (key0 <= full_hi) && (key0 > full_lo || key0 + kBtN <= a.n_sink);
+        tmem_wait_ld();
+        // logits in log2 units: the product is rounded here, once, so that the row
+        // maximum below is one of them and the winner's weight is 2^0 exactly
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const float f = mt->ks[q] * fac;
+#pragma unroll
+          for (int c = 16 * q; c < 16 * q + 16; c += 2) mul2(x[c], x[c + 1], f);
         }
-        // 64 columns at a time: factors and mask, and the row maximum
-        auto load_half = [&](int hf, float* x, float& mx) {
-          uint32_t* u = reinterpret_cast<uint32_t*>(x);
-          tmem_ld32(tS(s) + lane_off + 64 * hf, u);
-          tmem_ld32(tS(s) + lane_off + 64 * hf + 32, u + 32);
-          tmem_wait_ld();
-          if (full) {
+        if (!full) {
+          auto clip = [](int y) { return y < -1 ? -1 : (y > kBtN ? kBtN : y); };
+          const int lim = clip(gi - key0);
+          const int win_lo = a.window > 0 ? clip(gi - a.window - key0) : -1;
+          const int snk = a.window > 0 ? clip(a.n_sink - 1 - key0) : -1;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              float m2[2] = {x[16 * q], x[16 * q + 1]};
+          for (int c = 0; c < kBtN; ++c)
+            if (!(c <= lim && (c > win_lo || c <= snk))) x[c] = -INFINITY;
+        }
+        if (mt->vbad) {                         // NaN for the rows that see a marked key
+          for (int c = 0; c < kBtN; ++c)
+            if (((mt->vbad >> (c >> 4)) & 1) && key0 + c <= gi &&
+                (a.window == 0 || key0 + c > gi - a.window || key0 + c < a.n_sink))
+              poison = __uint_as_float(0x7fffffffu);
+        }
+        float m8[8];
 #pragma unroll
-              for (int c = 2; c < 16; c += 4) {
-                m2[0] = fmax3(m2[0], x[16 * q + c], c + 1 < 16 ? x[16 * q + c + 1] : m2[0]);
-                if (c + 2 < 16) m2[1] = fmax3(m2[1], x[16 * q + c + 2], x[16 * q + c + 3]);
-              }
-              mx = fmaxf(mx, fmaxf(m2[0], m2[1]) * (mt->ks[4 * hf + q] * fac));
-            }
-          } else {
+        for (int u = 0; u < 8; ++u) m8[u] = fmaxf(x[2 * u], x[2 * u + 1]);
 #pragma unroll
-            for (int c = 0; c < 64; ++c) {
-              const int col = 64 * hf + c;
-              const bool vis = col <= lim && (col > win_lo || col <= snk);
-              x[c] = vis ? x[c] * (mt->ks[4 * hf + (c >> 4)] * fac) : -INFINITY;
-              mx = fmaxf(mx, x[c]);
-            }
-          }
-        };
-        float l2[2] = {0.f, 0.f};
-        // weights of a half, packed in pairs; their sum goes to l2
-        auto exp_half = [&](int hf, const float* x, float mref, uint32_t* pc) {
+        for (int c = 16; c < kBtN; c += 16) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const int c = 2 * i;
-            float p0, p1;
-            if (full) {
-              const float f = mt->ks[4 * hf + (c >> 4)] * fac;
-              mul_add2(p0, p1, x[c], x[c + 1], f, -mref);
-              p0 = fast_exp2(p0);
-              p1 = fast_exp2(p1);
-            } else {
-              p0 = fast_exp2(x[c] - mref);
-              p1 = fast_exp2(x[c + 1] - mref);
-            }
-            l2[i & 1] += p0 + p1;
-            pc[i] = f2_to_h2(p0, p1);
-          }
-        };
-        float mx = -INFINITY;
-        float x[64];
-        load_half(0, x, mx);
-        load_half(1, x, mx);
+          for (int u = 0; u < 8; ++u) m8[u] = fmax3(m8[u], x[c + 2 * u], x[c + 2 * u + 1]);
+        }
+        const float mx = fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7]));
         const float m_new = fmaxf(m_used, mx);
         const bool need = m_new > m_used + kLazyRescale;
-        float alpha = 1.f;
+        float of = mt->vfac;                    // O's factor
+        vref = mt->vref;
         if (need) {
-          alpha = fast_exp2(m_used - m_new);     // 0 when m_used = -inf
+          const float alpha = fast_exp2(m_used - m_new);   // 0 when m_used = -inf
           m_used = m_new;
           l *= alpha;
+          of *= alpha;
         }
-        const float mref = (m_used == -INFINITY ? 0.f : m_used) - kKbUp;
-        // P of columns 64..127 goes where S of columns 64..127 is done with but S of
-        // 32..63 still stands: it waits in registers until that half is read again
-        uint32_t p_hi[32], p_lo[32];
-        exp_half(1, x, mref, p_hi);
-        float again = -INFINITY;
-        load_half(0, x, again);
-        tmem_st32(tS(s) + lane_off + 32, p_hi);
-        exp_half(0, x, mref, p_lo);
-        tmem_st32(tS(s) + lane_off, p_lo);
+        const float mref = kKbUp - (m_used == -INFINITY ? 0.f : m_used);
+        // weights, packed in pairs, over the columns of S as they are made
+        float l2[2] = {0.f, 0.f};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t pc[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int c = 32 * q + 2 * i;
+            add2(x[c], x[c + 1], mref, mref);
+            x[c] = fast_exp2(x[c]);
+            x[c + 1] = fast_exp2(x[c + 1]);
+            add2(l2[0], l2[1], x[c], x[c + 1]);
+            pc[i] = f2_to_h2(x[c], x[c + 1]);
+          }
+          tmem_st16(tS(s) + lane_off + 16 * q, pc);
+        }
         l += l2[0] + l2[1];
-        const float of = alpha * vfac;
         if (__any_sync(0xffffffffu, of != 1.f) && j > 0) {
 #pragma unroll 1
           for (int cb = 0; cb < D / 32; ++cb) {
@@ -532,11 +563,11 @@ __global__ void __launch_bounds__(kBtThreads, 1) attn_kv_block_tc_kernel(const _
       // ---- epilogue: O / l -> the output row, or a partial for the merge
       if (!(ok = __all_sync(0xffffffffu, mbar_wait(BAR(B_OFINAL + s), segs & 1, abort_flag)))) break;
       tc_fence_after();
-      const bool whole = w.whole();
+      const bool whole = w->whole;
       const float lse = l == 0.f ? -INFINITY : (m_used - kKbUp + log2f(l)) * 0.69314718055994530942f;
       const float inv = (l == 0.f ? 0.f : vref * ((KIND == 1 ? kE4m3Unscale : 1.f) / kBtVUp<KIND>) / l) + poison;
-      const int64_t prow = ((int64_t)blockIdx.x * 2 + w.slot()) * a.rows_item + s * kBtM + r;
-      const int64_t off = b * a.o.sb + (int64_t)tok * a.o.sn + (int64_t)hq * a.o.sh;
+      const int64_t prow = ((int64_t)blockIdx.x * 2 + w->slot) * a.rows_item + s * kBtM + r;
+      const int64_t off = (int64_t)w->b * a.o.sb + (int64_t)tok * a.o.sn + (int64_t)hq * a.o.sh;
 #pragma unroll 1
       for (int cb = 0; cb < D / 32; ++cb) {
         uint32_t o[32];
@@ -554,7 +585,7 @@ __global__ void __launch_bounds__(kBtThreads, 1) attn_kv_block_tc_kernel(const _
       }
       if (row_ok) {
         if (!whole) a.part_lse[prow] = lse;
-        else if (a.lse) a.lse[b * a.lse_sb + hq * a.lse_sh + tok] = lse;
+        else if (a.lse) a.lse[(int64_t)w->b * a.lse_sb + hq * a.lse_sh + tok] = lse;
       }
       tc_fence_before();                        // O is read before the next segment's MMAs write it (QREADY orders)
       jg += n;
