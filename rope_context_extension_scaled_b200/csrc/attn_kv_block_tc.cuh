@@ -285,13 +285,18 @@ __global__ void __launch_bounds__(kBtThreads, 1) attn_kv_block_tc_kernel(const _
     const KvBlockView& kv = a.c;
     const int lb = kv.block_log2, bmask = (1 << lb) - 1;
     constexpr int kRows = 128 / kPieces;          // key rows the 128 threads cover at once
-    const int pr = tid / kPieces, pc = tid % kPieces;
-    // a piece of 16 codes becomes two 16-byte chunks of one swizzled 128-byte row;
-    // pieces of the upper half store theirs in the other order (bank conflicts)
-    const int flip = (pc >> 2) & 1;
+    // Piece pc of key rows i * kRows + pr.  Eight lanes take four pieces of one
+    // 64-column half of two neighbouring rows: their 16-byte stores into the
+    // swizzled tile then fall into eight different bank groups.
+    const int pr = D == 128 ? (warp - kBtConv) * 4 + ((lane >> 2) & 1) + ((lane >> 4) << 1) : tid / 4;
+    const int pc = D == 128 ? (lane & 3) + ((lane >> 3) & 1) * 4 : tid % 4;
+    // a piece of 16 codes becomes the two 16-byte chunks 2 (pc % 4), + 1 of its row;
+    // row % 8 does not change with i
+    const uint32_t dst0 = (pc >> 2) * kBtHalf + pr * 128 + (((2 * (pc & 3)) ^ (pr & 7)) * 16);
     // a thread copies and converts the same pieces, so no barrier stands between
     const uint4* raw_k = reinterpret_cast<const uint4*>(smem + L::raw) + tid;
     const uint4* raw_v = raw_k + kPieces * 128;
+    const int64_t k_row = pr % 16 * kv.k_sn + pc * 16, v_row = pr % 16 * kv.v_sn + pc * 16;
     int jg = 0;
     while (ok && bt_next(w, a, lane)) {
       const int32_t* trow = kv.table + (int64_t)w->b * kv.t_sb;
@@ -322,30 +327,32 @@ __global__ void __launch_bounds__(kBtThreads, 1) attn_kv_block_tc_kernel(const _
       auto load_codes = [&](int u, int ph, const uint8_t* base, int64_t sb, int64_t sn, const uint4* raw) {
         if (u < u1) {
           const int key0 = w->span.tile(u) << kBtLogN;
+          const int rem = w->span.hi - key0 - pr;
+          const int64_t off = ph * sb + ((key0 + 16 * (lane & 7)) & bmask) * sn;   // of the lane's group
           const uint32_t dst = smem_addr(raw);
-#pragma unroll
+#pragma unroll 4
           for (int i = 0; i < kPieces; ++i) {
-            const int row = i * kRows + pr;
-            const int phys = __shfl_sync(0xffffffffu, ph, row >> 4);
-            const int bytes = key0 + row < w->span.hi ? 16 : 0;
-            const uint8_t* src = base + pc * 16 + (bytes ? phys * sb + ((key0 + row) & bmask) * sn : 0);
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + i * 2048), "l"(src), "r"(bytes)
+            const int64_t o = __shfl_sync(0xffffffffu, off, (i * kRows + pr) >> 4);
+            const int bytes = i * kRows < rem ? 16 : 0;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + i * 2048),
+                         "l"(bytes ? base + o : kv.k), "r"(bytes)
                          : "memory");
           }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
       };
       auto store_tile = [&](uint32_t tile_off, const uint4* raw, uint32_t ratios, auto scaled) {
-#pragma unroll
+        uint8_t* dst = smem + tile_off + dst0;
+        uint8_t* dst1 = smem + tile_off + (dst0 ^ 16);
+#pragma unroll 4
         for (int i = 0; i < kPieces; ++i) {
-          const int row = i * kRows + pr;
           const uint4 x = raw[i * 128];
           const uint32_t wv[4] = {x.x, x.y, x.z, x.w};
           uint32_t h[8];
 #pragma unroll
           for (int e = 0; e < 4; ++e) codes4_to_h2<KIND>(wv[e], h[2 * e], h[2 * e + 1]);
           if constexpr (decltype(scaled)::value) {
-            const uint32_t rb = __shfl_sync(0xffffffffu, ratios, 8 + (row >> 4));
+            const uint32_t rb = __shfl_sync(0xffffffffu, ratios, 8 + ((i * kRows + pr) >> 4));
             const __half2 rh = *reinterpret_cast<const __half2*>(&rb);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
@@ -353,15 +360,12 @@ __global__ void __launch_bounds__(kBtThreads, 1) attn_kv_block_tc_kernel(const _
               h[e] = *reinterpret_cast<const uint32_t*>(&y);
             }
           }
-          uint8_t* dst = smem + tile_off + (pc >> 2) * kBtHalf + row * 128;
-          const int c0 = (2 * (pc & 3) + flip) ^ (row & 7);
-          const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi4 = make_uint4(h[4], h[5], h[6], h[7]);
-          *reinterpret_cast<uint4*>(dst + c0 * 16) = flip ? hi4 : lo;
-          *reinterpret_cast<uint4*>(dst + (c0 ^ 1) * 16) = flip ? lo : hi4;
+          *reinterpret_cast<uint4*>(dst + i * kRows * 128) = make_uint4(h[0], h[1], h[2], h[3]);
+          *reinterpret_cast<uint4*>(dst1 + i * kRows * 128) = make_uint4(h[4], h[5], h[6], h[7]);
         }
       };
-      const uint8_t* kb = kv.k + w->hk * kv.k_sh;
-      const uint8_t* vb = kv.v + w->hk * kv.v_sh;
+      const uint8_t* kb = kv.k + w->hk * kv.k_sh + k_row;
+      const uint8_t* vb = kv.v + w->hk * kv.v_sh + v_row;
       const int u0 = w->u0;
       int ph_next = load_phys(u0 + 1);
       float sc;
