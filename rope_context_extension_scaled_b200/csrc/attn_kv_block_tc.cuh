@@ -11,11 +11,14 @@
 // heads fills the MMA's 128 rows at any group size.  512 threads:
 //   warps 0-3   softmax, Q load and epilogue of slot 0 (a thread per row)
 //   warps 4-7   the same of slot 1 (idle when an item has at most 128 rows)
-//   warps 8-11  converters: codes of the next tile are copied to shared memory
-//               (cp.async) while the current one is turned into fp16 and stored
-//               as 128B-swizzled K and V tiles (two stages), so the cache is
-//               read as it is stored, through its table, and never copied whole
-//   warp  12    MMA issuer and TMEM owner (13-15 have nothing to do)
+//   warps 8-11  converters: codes in shared memory -> fp16, stored as
+//               128B-swizzled K and V tiles (two stages)
+//   warp  12    MMA issuer and TMEM owner
+//   warp  13    producer: follows the table, copies the next tile's codes to
+//               shared memory (bulk copies of 16 tokens, or of a token where
+//               those are not contiguous) and works out its scales, so the
+//               cache is read as it is stored and never copied whole
+//   (14, 15 have nothing to do)
 // The softmax threads hold a row of S: registers move to them from the other
 // warpgroups (setmaxnreg; 2 x 200, 72 and 40 a thread are the launch's 65,536),
 // and each warp's place in the walk over segments is kept in shared memory.
@@ -47,8 +50,10 @@ constexpr int kBtRegsSoftmax = 200, kBtRegsConv = 72, kBtRegsMma = 40;
 static_assert(128 * (2 * kBtRegsSoftmax + kBtRegsConv + kBtRegsMma) <= 512 * 128, "registers of the launch");
 constexpr int kBtConv = 8;                      // first converter warp
 constexpr int kBtMma = 12;
+constexpr int kBtProd = 13;
+constexpr int kBtWalkers = 14;                  // warps that walk the segments
 constexpr int kBtStages = 2;
-constexpr int kBtMeta = 4;                      // ring of per-tile scales
+constexpr int kBtMeta = 8;                      // ring of per-tile scales
 constexpr uint32_t kBtHalf = kBtM * 128;        // 128 rows x 64 fp16, one swizzled block
 
 // The fp16 V tile holds value * this / (256 for e4m3) / (largest V scale): at
@@ -58,6 +63,7 @@ constexpr float kBtVUp = KIND == 0 ? 256.f : 32768.f;
 
 struct BtMeta {
   float ks[8];                                  // K scale of each 16 keys
+  uint32_t ratio[8];                            // V scale / vref * kBtVUp, an fp16 pair
   float vfac;                                   // O's factor before this tile is added
   uint32_t vbad;                                // 16-key groups with a non-finite V scale
   float vref;                                   // largest V scale so far
@@ -102,12 +108,20 @@ struct BtSmem {
   static constexpr uint32_t bar = raw + 2 * kBtN * D;
   static constexpr uint32_t meta = bar + 256;
   static constexpr uint32_t seg = meta + kBtMeta * sizeof(BtMeta);
-  static constexpr uint32_t total = seg + 13 * sizeof(BtSeg) + 1024;   // + alignment slack
+  static constexpr uint32_t total = seg + kBtWalkers * sizeof(BtSeg) + 1024;   // + alignment slack
 };
 
 // kind::f16 descriptor: fp16 A and B, fp32 accumulator, M = 128
 __host__ __device__ constexpr uint32_t idesc_f16(bool b_mn_major, int n) {
   return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kBtM >> 4) << 24);
+}
+
+// Bulk copy of `bytes` (16-byte aligned on both sides, a multiple of 16) that
+// completes on mbarrier `bar`.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
 }
 
 // Packed fp32 arithmetic: two values an instruction.
@@ -133,6 +147,7 @@ __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.
 template <int D, int KIND>
 __global__ void __launch_bounds__(kBtThreads, 1) attn_kv_block_tc_kernel(const __grid_constant__ KvAttnArgs a) {
   using L = BtSmem<D>;
+  static_assert(L::total <= 227 * 1024, "shared memory of a CTA");
   constexpr int kPieces = D / 16;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -149,7 +164,9 @@ __global__ void __launch_bounds__(kBtThreads, 1) attn_kv_block_tc_kernel(const _
     B_PREADY = B_SFULL + 2,           // [2] (128 arrivals)
     B_OFINAL = B_PREADY + 2,          // [2]
     B_META = B_OFINAL + 2,            // [ring] scales of a tile written (32 arrivals)
-    B_DRAIN = B_META + kBtMeta,
+    B_RFULL = B_META + kBtMeta,       // [K, V] codes of a tile landed
+    B_REMPTY = B_RFULL + 2,           // [K, V] they have been read (128 arrivals)
+    B_DRAIN = B_REMPTY + 2,
     B_NEVER,
     B_COUNT
   };
@@ -165,7 +182,7 @@ __global__ void __launch_bounds__(kBtThreads, 1) attn_kv_block_tc_kernel(const _
     for (int i = 0; i < B_COUNT; ++i) {
       uint32_t cnt = 1;
       if (i < 2 || (i >= B_KFULL && i < B_KFULL + kBtStages) || (i >= B_VFULL && i < B_VFULL + kBtStages) ||
-          i == B_PREADY || i == B_PREADY + 1)
+          i == B_PREADY || i == B_PREADY + 1 || i == B_REMPTY || i == B_REMPTY + 1)
         cnt = 128;
       if (i >= B_META && i < B_META + kBtMeta) cnt = 32;
       mbar_init(BAR(i), cnt);
@@ -176,7 +193,7 @@ __global__ void __launch_bounds__(kBtThreads, 1) attn_kv_block_tc_kernel(const _
   }
   if (warp == 0) {
     const PlanStart p = plan_start<kBtLogN>(a, blockIdx.x, lane);
-    if (lane < 13) {
+    if (lane < kBtWalkers) {
       BtSeg* g = segs_all + lane;
       g->e = p.e; g->off = p.off; g->x = g->x0 = p.x0; g->x1 = p.x1;
     }
@@ -190,7 +207,7 @@ __global__ void __launch_bounds__(kBtThreads, 1) attn_kv_block_tc_kernel(const _
   auto tS = [&](int s) { return tmem + 128u * (uint32_t)s; };
   auto tO = [&](int s) { return tmem + 256u + 128u * (uint32_t)s; };
   auto warp_wait = [&](int b, uint32_t par) { return __all_sync(0xffffffffu, mbar_wait(BAR(b), par, abort_flag)); };
-  BtSeg* const w = segs_all + min(warp, 12);
+  BtSeg* const w = segs_all + min(warp, kBtWalkers - 1);
   bool ok = true;
 
   if (warp >= kBtMma) {
@@ -277,110 +294,67 @@ __global__ void __launch_bounds__(kBtThreads, 1) attn_kv_block_tc_kernel(const _
     umma_commit_e(BAR(B_DRAIN));
     if (lane == 0) mbar_wait(BAR(B_DRAIN), 0, abort_flag, 100000000ull, false);
     __syncwarp();
-    }
-  } else if (warp >= kBtConv) {
-    // ================================================================ converters
-    regs_down<kBtRegsConv>();
-    const int tid = threadIdx.x - kBtConv * 32;
+    } else if (warp == kBtProd) {
+    // ================================================================ producer
     const KvBlockView& kv = a.c;
     const int lb = kv.block_log2, bmask = (1 << lb) - 1;
-    constexpr int kRows = 128 / kPieces;          // key rows the 128 threads cover at once
-    // Piece pc of key rows i * kRows + pr.  Eight lanes take four pieces of one
-    // 64-column half of two neighbouring rows: their 16-byte stores into the
-    // swizzled tile then fall into eight different bank groups.
-    const int pr = D == 128 ? (warp - kBtConv) * 4 + ((lane >> 2) & 1) + ((lane >> 4) << 1) : tid / 4;
-    const int pc = D == 128 ? (lane & 3) + ((lane >> 3) & 1) * 4 : tid % 4;
-    // a piece of 16 codes becomes the two 16-byte chunks 2 (pc % 4), + 1 of its row;
-    // row % 8 does not change with i
-    const uint32_t dst0 = (pc >> 2) * kBtHalf + pr * 128 + (((2 * (pc & 3)) ^ (pr & 7)) * 16);
-    // a thread copies and converts the same pieces, so no barrier stands between
-    const uint4* raw_k = reinterpret_cast<const uint4*>(smem + L::raw) + tid;
-    const uint4* raw_v = raw_k + kPieces * 128;
-    const int64_t k_row = pr % 16 * kv.k_sn + pc * 16, v_row = pr % 16 * kv.v_sn + pc * 16;
-    int jg = 0;
-    while (ok && bt_next(w, a, lane)) {
-      const int32_t* trow = kv.table + (int64_t)w->b * kv.t_sb;
-      const int u1 = w->u0 + w->n;
-      // lane i < 8: block of 16-key group i of tile u (0 behind the keys)
-      auto load_phys = [&](int u) {
-        int e = 0;
-        if (u < u1) {
-          const int key = (w->span.tile(u) << kBtLogN) + 16 * (lane & 7);
-          if (key < w->span.hi) {
-            e = trow[key >> lb];
-            if ((unsigned)e >= (unsigned)kv.n_blocks) {
-              record_device_error(RCX_ERR_DEVICE_INDEX);
-              e = 0;
-            }
+    const uint32_t raw = sbase + L::raw;
+    int jg = 0, sent[2] = {0, 0};                 // tiles; K and V tiles whose copies were issued
+    // lane i < 8: block of 16-key group i of tile u (0 behind the keys)
+    auto load_phys = [&](int u, int u1) {
+      int e = 0;
+      if (u < u1) {
+        const int key = (w->span.tile(u) << kBtLogN) + 16 * (lane & 7);
+        if (key < w->span.hi) {
+          e = kv.table[(int64_t)w->b * kv.t_sb + (key >> lb)];
+          if ((unsigned)e >= (unsigned)kv.n_blocks) {
+            record_device_error(RCX_ERR_DEVICE_INDEX);
+            e = 0;
           }
         }
-        return e;
-      };
-      // lanes 0-7 K, 8-15 V scale of the groups of tile u with blocks ph
-      auto load_scale = [&](int u, int ph) {
-        float s = 0.f;
-        if (u < u1 && lane < 16 && (w->span.tile(u) << kBtLogN) + 16 * (lane & 7) < w->span.hi)
-          s = (lane < 8 ? kv.ks : kv.vs)[(int64_t)ph * kv.Hkv + w->hk];
-        return s;
-      };
-      // codes of tile u -> the thread's raw pieces (keys behind the sequence: zeros, nothing read)
-      auto load_codes = [&](int u, int ph, const uint8_t* base, int64_t sb, int64_t sn, const uint4* raw) {
-        if (u < u1) {
-          const int key0 = w->span.tile(u) << kBtLogN;
-          const int rem = w->span.hi - key0 - pr;
-          const int64_t off = ph * sb + ((key0 + 16 * (lane & 7)) & bmask) * sn;   // of the lane's group
-          const uint32_t dst = smem_addr(raw);
-#pragma unroll 4
-          for (int i = 0; i < kPieces; ++i) {
-            const int64_t o = __shfl_sync(0xffffffffu, off, (i * kRows + pr) >> 4);
-            const int bytes = i * kRows < rem ? 16 : 0;
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + i * 2048),
-                         "l"(bytes ? base + o : kv.k), "r"(bytes)
-                         : "memory");
-          }
-        }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-      };
-      auto store_tile = [&](uint32_t tile_off, const uint4* raw, uint32_t ratios, auto scaled) {
-        uint8_t* dst = smem + tile_off + dst0;
-        uint8_t* dst1 = smem + tile_off + (dst0 ^ 16);
-#pragma unroll 4
-        for (int i = 0; i < kPieces; ++i) {
-          const uint4 x = raw[i * 128];
-          const uint32_t wv[4] = {x.x, x.y, x.z, x.w};
-          uint32_t h[8];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) codes4_to_h2<KIND>(wv[e], h[2 * e], h[2 * e + 1]);
-          if constexpr (decltype(scaled)::value) {
-            const uint32_t rb = __shfl_sync(0xffffffffu, ratios, 8 + ((i * kRows + pr) >> 4));
-            const __half2 rh = *reinterpret_cast<const __half2*>(&rb);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&h[e]), rh);
-              h[e] = *reinterpret_cast<const uint32_t*>(&y);
-            }
-          }
-          *reinterpret_cast<uint4*>(dst + i * kRows * 128) = make_uint4(h[0], h[1], h[2], h[3]);
-          *reinterpret_cast<uint4*>(dst1 + i * kRows * 128) = make_uint4(h[4], h[5], h[6], h[7]);
-        }
-      };
-      const uint8_t* kb = kv.k + w->hk * kv.k_sh + k_row;
-      const uint8_t* vb = kv.v + w->hk * kv.v_sh + v_row;
-      const int u0 = w->u0;
-      int ph_next = load_phys(u0 + 1);
-      float sc;
-      {
-        const int ph = load_phys(u0);
-        sc = load_scale(u0, ph);
-        load_codes(u0, ph, kb, kv.k_sb, kv.k_sn, raw_k);
-        load_codes(u0, ph, vb, kv.v_sb, kv.v_sn, raw_v);
       }
+      return e;
+    };
+    // lanes 0-7 K, 8-15 V scale of the groups of tile u with blocks ph
+    auto load_scale = [&](int u, int u1, int ph) {
+      float sc = 0.f;
+      if (u < u1 && lane < 16 && (w->span.tile(u) << kBtLogN) + 16 * (lane & 7) < w->span.hi)
+        sc = (lane < 8 ? kv.ks : kv.vs)[(int64_t)ph * kv.Hkv + w->hk];
+      return sc;
+    };
+    // codes of tile u's keys in the sequence -> raw rows; what stands in the other
+    // rows converts to finite numbers too, and their weights are zero
+    auto copy_codes = [&](int u, int ph, int isv) {
+      const uint8_t* base = isv ? kv.v + w->hk * kv.v_sh : kv.k + w->hk * kv.k_sh;
+      const int64_t sb = isv ? kv.v_sb : kv.k_sb, sn = isv ? kv.v_sn : kv.k_sn;
+      const uint32_t dst = raw + isv * kBtN * D, bar = BAR(B_RFULL + isv);
+      const int key0 = w->span.tile(u) << kBtLogN;
+      const int rows = min(w->span.hi - key0, kBtN);
+      const int64_t off = ph * sb + ((key0 + 16 * (lane & 7)) & bmask) * sn;     // of the lane's group
+      if (lane == 0) mbar_expect_tx(bar, rows * D);
+      __syncwarp();
+      if (sn == D) {
+        const int n = min(rows - 16 * lane, 16);
+        if (lane < 8 && n > 0) bulk_load(dst + 16 * lane * D, base + off, n * D, bar);
+      } else {
+        for (int i = 0; i < kBtN / 32; ++i) {
+          const int r = 32 * i + lane;
+          const int64_t o = __shfl_sync(0xffffffffu, off, r >> 4) + (r & 15) * sn;
+          if (r < rows) bulk_load(dst + r * D, base + o, D, bar);
+        }
+      }
+      ++sent[isv];
+    };
+    while (ok && bt_next(w, a, lane)) {
+      const int u0 = w->u0, u1 = u0 + w->n;
+      int ph = load_phys(u0, u1), ph_next = load_phys(u0 + 1, u1);
+      float sc = load_scale(u0, u1, ph);
       float vref = 0.f;
       for (int u = u0; u < u1; ++u, ++jg) {
-        const int st = jg % kBtStages;
-        const uint32_t par = ((jg / kBtStages) & 1) ^ 1;
-        const int ph_next2 = load_phys(u + 2);
-        const float sc_next = load_scale(u + 1, ph_next);
+        const int ph_next2 = load_phys(u + 2, u1);
+        const float sc_next = load_scale(u + 1, u1, ph_next);
+        if (!(ok = warp_wait(B_REMPTY, (jg & 1) ^ 1))) break;
+        copy_codes(u, ph, 0);
         // V scales: running maximum, ratios in fp16 (lanes 8-15 hold the groups')
         const bool is_v = lane >= 8 && lane < 16;
         const bool bad = is_v && !(fabsf(sc) < INFINITY);
@@ -388,37 +362,89 @@ __global__ void __launch_bounds__(kBtThreads, 1) attn_kv_block_tc_kernel(const _
         const float vmax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(sv, 0.f))));
         const uint32_t vbad = (__ballot_sync(0xffffffffu, bad) >> 8) & 0xffu;
         const float vnew = fmaxf(vref, vmax);
-        const float vfac = vnew > 0.f ? vref / vnew : 1.f;
-        vref = vnew;
-        const float ratio = vref > 0.f ? sv / vref * kBtVUp<KIND> : 0.f;
-        const uint32_t ratios = f2_to_h2(ratio, ratio);
-        asm volatile("cp.async.wait_group 1;" ::: "memory");   // K's codes
-        if (!(ok = warp_wait(B_KEMPTY + st, par))) break;
-        store_tile(L::k + st * L::tile, raw_k, 0u, std::false_type{});
-        if (warp == kBtConv) {                    // the tile's scales
-          BtMeta* mt = meta + jg % kBtMeta;
-          if (lane < 8) mt->ks[lane] = sc;
-          if (lane == 8) {
-            mt->vfac = vfac;
-            mt->vbad = vbad;
-            mt->vref = vref;
-          }
-          mbar_arrive(BAR(B_META + jg % kBtMeta));
+        const float ratio = vnew > 0.f ? sv / vnew * kBtVUp<KIND> : 0.f;
+        // the slot's last reader was the softmax of tile jg - 8: the copies above waited
+        // for K of jg - 1 to be read, so K of jg - 2 stands in its stage and S of jg - 4
+        // is done, which came after both slots' weights of jg - 5
+        BtMeta* mt = meta + jg % kBtMeta;
+        if (lane < 8) mt->ks[lane] = sc;
+        if (is_v) mt->ratio[lane - 8] = f2_to_h2(ratio, ratio);
+        if (lane == 0) {
+          mt->vfac = vnew > 0.f ? vref / vnew : 1.f;
+          mt->vbad = vbad;
+          mt->vref = vnew;
         }
-        fence_proxy_async_smem();
-        mbar_arrive(BAR(B_KFULL + st));
-        load_codes(u + 1, ph_next, kb, kv.k_sb, kv.k_sn, raw_k);
-        asm volatile("cp.async.wait_group 1;" ::: "memory");   // V's codes
-        if (!(ok = warp_wait(B_VEMPTY + st, par))) break;
-        store_tile(L::v + st * L::tile, raw_v, ratios, std::true_type{});
-        fence_proxy_async_smem();
-        mbar_arrive(BAR(B_VFULL + st));
-        load_codes(u + 1, ph_next, vb, kv.v_sb, kv.v_sn, raw_v);
+        vref = vnew;
+        mbar_arrive(BAR(B_META + jg % kBtMeta));
+        __syncwarp();
+        if (!(ok = warp_wait(B_REMPTY + 1, (jg & 1) ^ 1))) break;
+        copy_codes(u, ph, 1);                     // its arrival also publishes the ratios
+        ph = ph_next;
         ph_next = ph_next2;
         sc = sc_next;
       }
     }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    if (*abort_flag && lane == 0)                 // copies in flight land before the CTA ends
+      for (int i = 0; i < 2; ++i)
+        if (sent[i]) mbar_wait(BAR(B_RFULL + i), (sent[i] - 1) & 1, abort_flag, 100000000ull, false);
+    __syncwarp();
+    }
+  } else if (warp >= kBtConv) {
+    // ================================================================ converters
+    regs_down<kBtRegsConv>();
+    const int tid = threadIdx.x - kBtConv * 32;
+    constexpr int kRows = 128 / kPieces;          // key rows the 128 threads cover at once
+    // Piece pc of key rows i * kRows + pr.  Eight lanes take the pieces of one half
+    // of a row and of the other half of the next: their 16-byte reads, and their
+    // stores into the swizzled tile, fall into eight different bank groups.
+    const int pr = D == 128 ? (warp - kBtConv) * 4 + ((lane >> 2) & 1) + ((lane >> 4) << 1) : tid / 4;
+    const int pc = D == 128 ? (lane & 3) + (((lane >> 3) ^ (lane >> 2)) & 1) * 4 : tid % 4;
+    // a piece of 16 codes becomes the two 16-byte chunks 2 (pc % 4), + 1 of its row;
+    // row % 8 does not change with i
+    const uint32_t dst0 = (pc >> 2) * kBtHalf + pr * 128 + (((2 * (pc & 3)) ^ (pr & 7)) * 16);
+    const uint4* raw_k = reinterpret_cast<const uint4*>(smem + L::raw + pr * D + pc * 16);
+    const uint4* raw_v = raw_k + kBtN * D / 16;
+    auto store_tile = [&](uint32_t tile_off, const uint4* raw, const uint32_t* ratios, auto scaled) {
+      uint8_t* dst = smem + tile_off + dst0;
+      uint8_t* dst1 = smem + tile_off + (dst0 ^ 16);
+#pragma unroll 2
+      for (int i = 0; i < kPieces; ++i) {
+        const uint4 x = raw[i * kRows * D / 16];
+        const uint32_t wv[4] = {x.x, x.y, x.z, x.w};
+        uint32_t h[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) codes4_to_h2<KIND>(wv[e], h[2 * e], h[2 * e + 1]);
+        if constexpr (decltype(scaled)::value) {
+          const uint32_t rb = ratios[(i * kRows + pr) >> 4];
+          const __half2 rh = *reinterpret_cast<const __half2*>(&rb);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&h[e]), rh);
+            h[e] = *reinterpret_cast<const uint32_t*>(&y);
+          }
+        }
+        *reinterpret_cast<uint4*>(dst + i * kRows * 128) = make_uint4(h[0], h[1], h[2], h[3]);
+        *reinterpret_cast<uint4*>(dst1 + i * kRows * 128) = make_uint4(h[4], h[5], h[6], h[7]);
+      }
+    };
+    int jg = 0;
+    while (ok && bt_next(w, a, lane)) {
+      const int end = jg + w->n;
+      for (; jg < end; ++jg) {
+        const int st = jg % kBtStages;
+        const uint32_t par = ((jg / kBtStages) & 1) ^ 1;
+        if (!(ok = warp_wait(B_KEMPTY + st, par) && warp_wait(B_RFULL, jg & 1))) break;
+        store_tile(L::k + st * L::tile, raw_k, nullptr, std::false_type{});
+        fence_proxy_async_smem();
+        mbar_arrive(BAR(B_KFULL + st));
+        mbar_arrive(BAR(B_REMPTY));
+        if (!(ok = warp_wait(B_VEMPTY + st, par) && warp_wait(B_RFULL + 1, jg & 1))) break;
+        store_tile(L::v + st * L::tile, raw_v, meta[jg % kBtMeta].ratio, std::true_type{});
+        fence_proxy_async_smem();
+        mbar_arrive(BAR(B_VFULL + st));
+        mbar_arrive(BAR(B_REMPTY + 1));
+      }
+    }
   } else {
     // ================================================================ softmax + epilogue
     regs_up<kBtRegsSoftmax>();
