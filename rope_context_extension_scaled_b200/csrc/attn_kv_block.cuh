@@ -33,7 +33,7 @@
 
 namespace rcx {
 
-constexpr int kKbWarps = 4;
+constexpr int kKbWarps = kKvFewWarps;
 constexpr int kKbStages = 3;
 constexpr int kKbKeys = kKvFewTile;             // keys per tile
 constexpr int kKbCtasPerSm = kKvFewCtasPerSm;
@@ -61,14 +61,6 @@ __device__ __forceinline__ void row_pow2(uint32_t bits, float& up, float& down) 
   down = __uint_as_float((uint32_t)(254 - f) << 23);
 }
 
-// One output row piece of 4 dims (16-byte aligned in fp32, 8-byte in bf16).
-__device__ __forceinline__ void store_o4(const KvAttnArgs& a, int64_t off, float4 x) {
-  if (a.o_bf16)
-    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o.ptr) + off) = make_uint2(f2_to_bf2(x.x, x.y), f2_to_bf2(x.z, x.w));
-  else
-    *reinterpret_cast<float4*>(static_cast<float*>(a.o.ptr) + off) = x;
-}
-
 template <int D, int NT, int KIND>
 __global__ void __launch_bounds__(kKbWarps * 32, kKbCtasPerSm) attn_kv_block_kernel(const KvAttnArgs a) {
   constexpr int LOGT = 5;
@@ -90,6 +82,7 @@ __global__ void __launch_bounds__(kKbWarps * 32, kKbCtasPerSm) attn_kv_block_ker
     const PlanStart p = plan_start<LOGT>(a, blockIdx.x, lane);
     if (lane == 0) sm_plan = p;
   }
+  if (a.direct) empty_rows<D>(a, warp, kKbWarps, lane);
   __syncthreads();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   SegWalk w;

@@ -199,6 +199,7 @@ __global__ void __launch_bounds__(kBtThreads, 1) attn_kv_block_tc_kernel(const _
     }
   }
   if (warp == kBtMma) tmem_alloc(smem_addr(tmem_slot), 512);
+  if (a.direct) empty_rows<D>(a, warp, kBtThreads / 32, lane);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();

@@ -43,7 +43,8 @@ struct KvAttnArgs {
   int o_bf16;
   int rows_item;                    // rows (token, head of the group) an item holds
   int n_rt;                         // items a (sequence, KV head) has at most
-  int n_cta;                        // CTAs the key tiles are dealt to
+  int n_cta;                        // CTAs the key tiles (direct: items) are dealt to
+  int direct;                       // items are not cut: no partials, no merge
   float* part_o;                    // [n_cta, 2, rows_item, d]: partials of items that several CTAs share
   float* part_lse;                  // [n_cta, 2, rows_item]
   int* prefix;                      // [B * n_rt + 1] first key tile of each (sequence, row tile)

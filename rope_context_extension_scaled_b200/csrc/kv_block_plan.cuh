@@ -10,10 +10,22 @@
 // load the P CTAs evenly, and only items that a CTA border cuts need a merge.
 // Heads are the fastest index: CTAs that run side by side on one sequence read
 // the same head's keys.
+//
+// Where items are short, or plenty and alike, cutting them costs more than it
+// evens out: then (direct) the line is dealt out by whole items, there is
+// nothing to scan and nothing to merge.
 #pragma once
 #include "kv_block.cuh"
 
 namespace rcx {
+
+// One output row piece of 4 dims (16-byte aligned in fp32, 8-byte in bf16).
+__device__ __forceinline__ void store_o4(const KvAttnArgs& a, int64_t off, float4 x) {
+  if (a.o_bf16)
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o.ptr) + off) = make_uint2(f2_to_bf2(x.x, x.y), f2_to_bf2(x.z, x.w));
+  else
+    *reinterpret_cast<float4*>(static_cast<float*>(a.o.ptr) + off) = x;
+}
 
 // Key tiles (2^LOGT keys each) that rows of tokens n_lo .. n_hi may see.
 struct KeySpan {
@@ -69,7 +81,7 @@ __device__ __forceinline__ int range_start(int T, int i, int P) { return (int)((
 __device__ __forceinline__ int range_owner(int T, int x, int P) { return (int)((((int64_t)x + 1) * P - 1) / T); }
 
 // Where a CTA begins: entry e, tile `off` of its Hkv * span.n tiles, and the
-// CTA's range [x0, x1).
+// CTA's range [x0, x1) (direct: of items).
 struct PlanStart {
   int e, off, x0, x1;
 };
@@ -79,6 +91,12 @@ template <int LOGT>
 __device__ __forceinline__ PlanStart plan_start(const KvAttnArgs& a, int cta, int lane) {
   const int E = a.B * a.n_rt, Hkv = a.c.Hkv;
   PlanStart p;
+  if (a.direct) {
+    p.e = p.off = 0;
+    p.x0 = range_start(E * Hkv, cta, a.n_cta);
+    p.x1 = range_start(E * Hkv, cta + 1, a.n_cta);
+    return p;
+  }
   int carry = 0, incl = 0, mine = 0;
   for (int e0 = 0; e0 < E; e0 += 32) {
     const int e = e0 + lane;
@@ -138,6 +156,18 @@ struct SegWalk {
   }
   template <int LOGT>
   __device__ __forceinline__ bool next(const KvAttnArgs& a) {
+    if (a.direct) {
+      while (x < x1) {
+        const int i = x++;
+        e = i / a.c.Hkv;
+        hk = i - e * a.c.Hkv;
+        t = entry_of<LOGT>(a, e);
+        u0 = 0;
+        u1 = t.span.n;
+        if (u1 > 0) return true;
+      }
+      return false;
+    }
     const int E = a.B * a.n_rt;
     while (x < x1 && e < E) {
       if (!fresh) {
@@ -163,5 +193,21 @@ struct SegWalk {
   __device__ __forceinline__ int slot() const { return x - (u1 - u0) == x0 ? 0 : 1; }
   __device__ __forceinline__ bool whole() const { return u0 == 0 && u1 == t.span.n; }
 };
+
+// O = 0 and LSE = -inf for the rows of tokens past a sequence's count (direct
+// launches; the merge writes them otherwise).  A warp per token.
+template <int D>
+__device__ __forceinline__ void empty_rows(const KvAttnArgs& a, int warp, int n_warps, int lane) {
+  for (int64_t i = (int64_t)blockIdx.x * n_warps + warp; i < (int64_t)a.B * a.N; i += (int64_t)gridDim.x * n_warps) {
+    const int64_t b = a.b0 + i / a.N, n = i % a.N;
+    if (n < seq_range(a.start, a.count, (int)b, a.N, a.c.cap).n) continue;
+    const int H = (int)a.q.H;
+    for (int x = lane; x < H * (D / 4); x += 32) {
+      const int h = x / (D / 4), dd = 4 * (x % (D / 4));
+      store_o4(a, b * a.o.sb + n * a.o.sn + h * a.o.sh + dd, make_float4(0.f, 0.f, 0.f, 0.f));
+      if (dd == 0 && a.lse) a.lse[b * a.lse_sb + h * a.lse_sh + n] = -INFINITY;
+    }
+  }
+}
 
 }  // namespace rcx

@@ -82,8 +82,11 @@ int kv_block_read_launch(const KvReadArgs& a, int dtype, int kind, dim3 grid, cu
 constexpr int kKvFewRows = 32;         // rows (tokens x heads of a group) up to which the mma.sync kernel runs
 constexpr int kKvFewTile = 32;         // its key tile and resident CTAs
 constexpr int kKvFewCtasPerSm = 2;
+constexpr int kKvFewWarps = 4;         // warps of its CTA, a tile each
+constexpr int kKvFewMergeTiles = 8;    // what a scan and a merge cost, in tile times (see kv_attn_impl)
 constexpr int kKvTcRows = 256;         // rows of an item of the tcgen05 kernel, and its key tile
 constexpr int kKvTcTile = 128;
+constexpr int kKvTcMergeTiles = 3;
 constexpr int kKvMaxSlice = 4096;      // sequences a launch takes
 constexpr int kKvReadPerCta = 512;     // 16-code pieces a CTA of the read kernel takes
 int attn_kv_block_launch_int8(const KvAttnArgs& a, cudaStream_t stream);

@@ -791,13 +791,28 @@ int kv_attn_impl(const rcx_tensor& q, const rcx_kv_blocks* cache, const int64_t*
   a.part_lse = reinterpret_cast<float*>(ws + p.off_lse);
   a.prefix = reinterpret_cast<int*>(ws + p.off_prefix);
   a.inject_spins = p.few ? 0 : attn_tc_inject();
+  // Most key tiles an item can have: all its rows' windows and the sinks.
+  const int64_t tile = p.few ? kKvFewTile : kKvTcTile;
+  const int64_t rows_tok = p.few ? N : std::min<int64_t>(N, kKvTcRows / a.G + 2);
+  int64_t reach = a.c.cap;
+  if (window > 0 && window < reach) reach = std::min<int64_t>(reach, window + rows_tok + a.n_sink + 2 * tile);
+  const int64_t most = (reach + tile - 1) / tile;
+  const int64_t lanes = p.few ? kKvFewWarps : 1;            // tiles a CTA works on at once
+  const int64_t ctas = (int64_t)sm_count() * (p.few ? kKvFewCtasPerSm : 1);
   for (int64_t b0 = 0; b0 < B; b0 += p.slice) {
     a.b0 = (int)b0;
     a.B = (int)std::min<int64_t>(B - b0, p.slice);
+    // Whole items against cut ones, in tile times of a CTA: the longest CTA's
+    // items, against an even share and what the scan and the merge cost.
+    const int64_t items = (int64_t)a.B * p.n_rt * a.c.Hkv;
+    const int64_t per_item = (most + lanes - 1) / lanes;
+    a.direct = (items + ctas - 1) / ctas * per_item <=
+               items * most / (ctas * lanes) + (p.few ? kKvFewMergeTiles : kKvTcMergeTiles);
+    a.n_cta = a.direct ? (int)std::min<int64_t>(ctas, items) : p.n_cta;
     st = !p.few ? attn_kv_block_tc_launch(a, kind, stream)
          : kind == 0 ? attn_kv_block_launch_int8(a, stream) : attn_kv_block_launch_e4m3(a, stream);
     if (st) return st;
-    if ((st = attn_kv_block_merge_launch(a, stream))) return st;
+    if (!a.direct && (st = attn_kv_block_merge_launch(a, stream))) return st;
   }
   return RCX_OK;
 }
