@@ -34,16 +34,16 @@
 namespace rcx {
 
 constexpr int kKbWarps = kKvFewWarps;
-constexpr int kKbStages = 3;
 constexpr int kKbKeys = kKvFewTile;             // keys per tile
-constexpr int kKbCtasPerSm = kKvFewCtasPerSm;
 constexpr float kKbLazy = 8.f;                  // log2 units a logit may pass m
 constexpr float kKbUp = 7.f;                    // P is held times 2^7
 
 template <int D>
 constexpr int kb_stage_bytes = 2 * kKbKeys * D;
 template <int D, int NT>
-constexpr int kb_smem_bytes = kKbWarps * kKbStages * kb_stage_bytes<D> + NT * (D / 16) * 32 * 8 + NT * 8 * 4;
+constexpr int kb_stages = kv_few_stages(D, NT);
+template <int D, int NT>
+constexpr int kb_smem_bytes = kKbWarps * kb_stages<D, NT> * kb_stage_bytes<D> + NT * (D / 16) * 32 * 8 + NT * 8 * 4;
 
 // 16-byte piece p of key row r sits at piece p ^ kb_swz(r): conflict-free for
 // the 8-row ldmatrix reads and for the quarter-warp reads of two rows.
@@ -62,11 +62,12 @@ __device__ __forceinline__ void row_pow2(uint32_t bits, float& up, float& down) 
 }
 
 template <int D, int NT, int KIND>
-__global__ void __launch_bounds__(kKbWarps * 32, kKbCtasPerSm) attn_kv_block_kernel(const KvAttnArgs a) {
+__global__ void __launch_bounds__(kKbWarps * 32, kv_few_ctas(D, NT)) attn_kv_block_kernel(const KvAttnArgs a) {
   constexpr int LOGT = 5;
   static_assert(1 << LOGT == kKbKeys, "tile");
   constexpr int kChunks = D / 16;               // 16-dim MMA steps
   constexpr int kStage = kb_stage_bytes<D>;
+  constexpr int kKbStages = kb_stages<D, NT>;
   constexpr int kTile = kKbKeys * D;
   constexpr int kPieces = D / 16;               // 16-byte pieces per key row
   constexpr int kRowsPerCopy = 32 / kPieces;    // key rows one warp-wide 16-byte copy covers
@@ -437,8 +438,10 @@ __global__ void __launch_bounds__(kKbWarps * 32, kKbCtasPerSm) attn_kv_block_ker
 // Merge of items that several CTAs share, by the LSE rule of rcx_merge_partials,
 // and zeros (LSE -inf) for the rows of tokens past a sequence's count.  One CTA
 // per (entry, KV head) and slice of its rows; kWarpsPerRow warps share a row's
-// partials.  Waits for the attention kernel's end on the device (programmatic
-// dependent launch), so that its launch is hidden behind it.
+// partials.  A warp reads 32 partials' LSE at once, then weighs their rows with
+// eight loads in flight: bound by the latency of that chain.  It waits for the
+// attention kernel's end on the device (programmatic dependent launch), so that
+// its launch is hidden behind it.
 template <int D, int kWarpsPerRow>
 static __global__ void __launch_bounds__(256) attn_kv_block_merge_kernel(const KvAttnArgs a) {
   constexpr int kL = D / 4;                      // lanes that hold dims (d = 64: half a warp)
@@ -446,8 +449,7 @@ static __global__ void __launch_bounds__(256) attn_kv_block_merge_kernel(const K
   __shared__ float4 sm_o[8][32];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int e = blockIdx.x, hk = blockIdx.y;
-  const int E = a.B * a.n_rt;
-  const int T = a.prefix[E], p0 = a.prefix[e];
+  const int T = a.prefix[a.B * a.n_rt], p0 = a.prefix[e];
   const int nt = (a.prefix[e + 1] - p0) / a.c.Hkv;
   const int rt = a.n_rt == 1 ? 0 : e % a.n_rt;
   const int64_t b = a.b0 + (a.n_rt == 1 ? e : e / a.n_rt);
@@ -455,8 +457,19 @@ static __global__ void __launch_bounds__(256) attn_kv_block_merge_kernel(const K
   const int r0 = rt * a.rows_item;
   const int live = max(0, min(s.n * a.G - r0, a.rows_item));
   const int rows = min(a.N * a.G - r0, a.rows_item);
-  const int i0 = p0 + hk * nt, i1 = i0 + nt;
-  const int c0 = nt > 0 ? range_owner(T, i0, a.n_cta) : 0, c1 = nt > 0 ? range_owner(T, i1 - 1, a.n_cta) : 0;
+  // CTAs c0 .. c1 hold pieces of the item; the first one's may be its range's last
+  // segment (the line), all others are their CTA's first
+  const int even = a.prefix[a.B * a.n_rt + 1];
+  int c0 = 0, c1 = 0, first_slot = 0;
+  if (nt > 0 && even > 0) {
+    c0 = (e * a.c.Hkv + hk) * even;
+    c1 = nt == 1 ? c0 : c0 + even - 1;       // a single tile is one whole piece
+  } else if (nt > 0) {
+    const int P = range_ctas(T, a), i0 = p0 + hk * nt;
+    c0 = range_owner(T, i0, P);
+    c1 = range_owner(T, i0 + nt - 1, P);
+    first_slot = range_start(T, c0, P) == i0 ? 0 : 1;
+  }
   if (live == rows && c0 == c1) return;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int team = warp / kWarpsPerRow, sub = warp % kWarpsPerRow;
@@ -465,25 +478,37 @@ static __global__ void __launch_bounds__(256) attn_kv_block_merge_kernel(const K
   for (int rb = blockIdx.z * kTeams; rb < rows; rb += gridDim.z * kTeams) {
     const int r = rb + team;
     const bool row_ok = r < rows;
-    const int n = (r0 + r) / a.G, hq = hk * a.G + (r0 + r) - n * a.G;
-    const int64_t off = b * a.o.sb + (int64_t)n * a.o.sn + (int64_t)hq * a.o.sh + dd;
+    const bool shared = row_ok && r < live && c0 != c1;
     float mm = -INFINITY, lsum = 0.f;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    const bool shared = row_ok && r < live && c0 != c1;
     if (shared) {
-      for (int c = c0 + sub; c <= c1; c += kWarpsPerRow) {
-        const int xc = range_start(T, c, a.n_cta);
-        if (xc == range_start(T, c + 1, a.n_cta)) continue;          // a CTA without tiles
-        const int64_t pr = ((int64_t)c * 2 + (xc >= i0 ? 0 : 1)) * a.rows_item + r;
-        const float ls = a.part_lse[pr];
-        const float4 y = *reinterpret_cast<const float4*>(a.part_o + pr * D + dd);
-        const float mn = fmaxf(mm, ls);                              // NaN stays in lsum and x
+      for (int cb = c0 + sub; cb <= c1; cb += 32 * kWarpsPerRow) {
+        const int c = cb + kWarpsPerRow * lane;
+        const int n = min(32, (c1 - cb) / kWarpsPerRow + 1);
+        const int64_t pr = ((int64_t)c * 2 + (c == c0 ? first_slot : 0)) * a.rows_item + r;
+        // (even: an item with fewer tiles than pieces leaves some without any)
+        const bool there = lane < n && (even == 0 || range_start(nt, c - c0, even) < range_start(nt, c - c0 + 1, even));
+        const float ls = there ? a.part_lse[pr] : -INFINITY;
+        float mn = ls;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));   // passes NaN over
+        mn = fmaxf(mn, mm);
+        const float wt = ls == -INFINITY ? 0.f : expf(ls - (mn == -INFINITY ? 0.f : mn));        // NaN stays here
         const float f0 = mm == mn ? 1.f : expf(mm - mn);
-        const float f1 = ls == -INFINITY ? 0.f : expf(ls - (mn == -INFINITY ? 0.f : mn));
-        x.x = x.x * f0 + f1 * y.x; x.y = x.y * f0 + f1 * y.y;
-        x.z = x.z * f0 + f1 * y.z; x.w = x.w * f0 + f1 * y.w;
-        lsum = lsum * f0 + f1;
+        float ws = wt;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) ws += __shfl_xor_sync(0xffffffffu, ws, o);
+        lsum = lsum * f0 + ws;
+        x.x *= f0; x.y *= f0; x.z *= f0; x.w *= f0;
         mm = mn;
+#pragma unroll 8
+        for (int i = 0; i < n; ++i) {
+          const float wi = __shfl_sync(0xffffffffu, wt, i);
+          const int64_t pi = __shfl_sync(0xffffffffu, pr, i);
+          if (wi == 0.f) continue;
+          const float4 y = *reinterpret_cast<const float4*>(a.part_o + pi * D + dd);
+          x.x += wi * y.x; x.y += wi * y.y; x.z += wi * y.z; x.w += wi * y.w;
+        }
       }
     }
     if constexpr (kWarpsPerRow > 1) {
@@ -501,20 +526,21 @@ static __global__ void __launch_bounds__(256) attn_kv_block_merge_kernel(const K
         lsum = 0.f;
 #pragma unroll
         for (int i = 0; i < kWarpsPerRow; ++i) {
-          const float f = sm_l[warp + i] == 0.f ? 0.f : expf(sm_m[warp + i] - (mt == -INFINITY ? 0.f : mt));
+          if (sm_l[warp + i] == 0.f) continue;
+          const float f = expf(sm_m[warp + i] - (mt == -INFINITY ? 0.f : mt));
           const float4 y = sm_o[warp + i][lane];
-          if (f != 0.f || sm_l[warp + i] != 0.f) {
-            x.x += f * y.x; x.y += f * y.y; x.z += f * y.z; x.w += f * y.w;
-            lsum += f * sm_l[warp + i];
-          }
+          x.x += f * y.x; x.y += f * y.y; x.z += f * y.z; x.w += f * y.w;
+          lsum += f * sm_l[warp + i];
         }
         mm = mt;
       }
       __syncthreads();
     }
     if (sub == 0 && row_ok && lane < kL && (shared || r >= live)) {
+      const int n = (r0 + r) / a.G, hq = hk * a.G + (r0 + r) - n * a.G;
       const float inv = lsum == 0.f ? 0.f : 1.f / lsum;
-      store_o4(a, off, make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv));
+      store_o4(a, b * a.o.sb + (int64_t)n * a.o.sn + (int64_t)hq * a.o.sh + dd,
+               make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv));
       if (lane == 0 && a.lse) a.lse[b * a.lse_sb + hq * a.lse_sh + n] = lsum == 0.f ? -INFINITY : mm + logf(lsum);
     }
   }

@@ -72,7 +72,7 @@ struct BtMeta {
 
 // A warp's place in the walk (e, off, x: see SegWalk) and its current segment.
 struct BtSeg {
-  int e, off, x, x0, x1;
+  int e, off, x, x0, x1, even;
   int ok;                                       // a segment is there
   int b, hk, r0, rows, start;
   KeySpan span;
@@ -84,7 +84,7 @@ __device__ __forceinline__ bool bt_next(BtSeg* g, const KvAttnArgs& a, int lane)
   __syncwarp();                                 // the old segment has been read
   if (lane == 0) {
     SegWalk w;
-    w.e = g->e; w.off = g->off; w.x = g->x; w.x0 = g->x0; w.x1 = g->x1;
+    w.e = g->e; w.off = g->off; w.x = g->x; w.x0 = g->x0; w.x1 = g->x1; w.even = g->even;
     w.fresh = false;
     g->ok = w.next<kBtLogN>(a);
     if (g->ok) {
@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(kBtThreads, 1) attn_kv_block_tc_kernel(const _
     const PlanStart p = plan_start<kBtLogN>(a, blockIdx.x, lane);
     if (lane < kBtWalkers) {
       BtSeg* g = segs_all + lane;
-      g->e = p.e; g->off = p.off; g->x = g->x0 = p.x0; g->x1 = p.x1;
+      g->e = p.e; g->off = p.off; g->x = g->x0 = p.x0; g->x1 = p.x1; g->even = p.even;
     }
   }
   if (warp == kBtMma) tmem_alloc(smem_addr(tmem_slot), 512);

@@ -1,5 +1,6 @@
 // Launchers of the tensor-core attention over the block-scaled KV cache
 // (attn_kv_block_tc.cuh) and of the merge of partials (attn_kv_block.cuh).
+#include <algorithm>
 #include "launch.h"
 #include "attn_kv_block_tc.cuh"
 
@@ -19,13 +20,17 @@ int attn_kv_block_tc_launch(const KvAttnArgs& a, int kind, cudaStream_t stream) 
   return kind == 0 ? kb_tc_launch<128, 0>(a, stream) : kb_tc_launch<128, 1>(a, stream);
 }
 
-// Few rows: a CTA of eight warps per row (an item's partials may come from
-// every CTA); many rows: a warp per row (an item is cut once or twice).
+// Where CTAs are many times the items, so are their partials: eight warps share a
+// row's.  Otherwise an item is cut a few times: a warp a row, with as many CTAs
+// an item as fill the GPU once.
 int attn_kv_block_merge_launch(const KvAttnArgs& a, cudaStream_t stream) {
   LaunchScope scope(RCX_KERNEL_DECODE, stream);
-  const bool few = a.rows_item <= kKvFewRows;
+  const int64_t items = (int64_t)a.B * a.n_rt * a.c.Hkv;
+  const bool many = items * 16 <= a.n_cta;
+  const int rows = std::min(a.N * a.G, a.rows_item);
+  const int z = many ? rows : (int)std::min<int64_t>((rows + 7) / 8, std::max<int64_t>(4, 8 * sm_count() / items));
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(a.B * a.n_rt), (unsigned)a.c.Hkv, few ? (unsigned)(a.N * a.G) : 4u);
+  cfg.gridDim = dim3((unsigned)(a.B * a.n_rt), (unsigned)a.c.Hkv, (unsigned)z);
   cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
@@ -33,8 +38,8 @@ int attn_kv_block_merge_launch(const KvAttnArgs& a, cudaStream_t stream) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  auto kern = a.q.D == 64 ? (few ? attn_kv_block_merge_kernel<64, 8> : attn_kv_block_merge_kernel<64, 1>)
-                          : (few ? attn_kv_block_merge_kernel<128, 8> : attn_kv_block_merge_kernel<128, 1>);
+  auto kern = a.q.D == 64 ? (many ? attn_kv_block_merge_kernel<64, 8> : attn_kv_block_merge_kernel<64, 1>)
+                          : (many ? attn_kv_block_merge_kernel<128, 8> : attn_kv_block_merge_kernel<128, 1>);
   if (cudaLaunchKernelEx(&cfg, kern, a) != cudaSuccess) {
     launch_status();
     return RCX_ERR_CUDA;

@@ -44,10 +44,12 @@ struct KvAttnArgs {
   int rows_item;                    // rows (token, head of the group) an item holds
   int n_rt;                         // items a (sequence, KV head) has at most
   int n_cta;                        // CTAs the key tiles (direct: items) are dealt to
+  int min_tiles;                    // key tiles a CTA takes at least
+  int start_tiles;                  // tiles' worth of time that beginning an item costs
   int direct;                       // items are not cut: no partials, no merge
   float* part_o;                    // [n_cta, 2, rows_item, d]: partials of items that several CTAs share
   float* part_lse;                  // [n_cta, 2, rows_item]
-  int* prefix;                      // [B * n_rt + 1] first key tile of each (sequence, row tile)
+  int* prefix;                      // [B * n_rt + 2] first key tile of each (sequence, row tile); pieces of an item
   int64_t inject_spins;             // test hook of the tensor-core kernel
 };
 

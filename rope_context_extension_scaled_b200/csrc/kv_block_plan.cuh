@@ -11,9 +11,14 @@
 // Heads are the fastest index: CTAs that run side by side on one sequence read
 // the same head's keys.
 //
-// Where items are short, or plenty and alike, cutting them costs more than it
-// evens out: then (direct) the line is dealt out by whole items, there is
-// nothing to scan and nothing to merge.
+// Beginning an item costs a CTA about start_tiles tiles (its queries, its first
+// table entries and keys, its end), so two cases are dealt out otherwise:
+//   even:    fewer items than CTAs, and alike: each item is cut into `even` equal
+//            pieces, one a CTA, where the largest piece is within start_tiles of
+//            an even share;
+//   direct:  items too short to be worth cutting (decided on the host, which
+//            knows how long they can be): the line holds whole items, and there
+//            is nothing to scan and nothing to merge.
 #pragma once
 #include "kv_block.cuh"
 
@@ -75,15 +80,24 @@ __device__ __forceinline__ Entry entry_of(const KvAttnArgs& a, int e) {
   return t;
 }
 
+// CTAs that T tiles go to: as many as there are, each with min_tiles at least.
+__device__ __forceinline__ int range_ctas(int T, const KvAttnArgs& a) { return max(1, min(a.n_cta, T / a.min_tiles)); }
 // First tile of CTA i.
 __device__ __forceinline__ int range_start(int T, int i, int P) { return (int)((int64_t)T * i / P); }
 // The CTA whose range holds tile x (the last i with range_start(i) <= x).
 __device__ __forceinline__ int range_owner(int T, int x, int P) { return (int)((((int64_t)x + 1) * P - 1) / T); }
 
+// Pieces of each item (0: the line is cut), from the T tiles of `items` items of
+// at most `most` tiles each.
+__device__ __forceinline__ int even_pieces(const KvAttnArgs& a, int T, int items, int most) {
+  const int s = min(a.n_cta / items, max(1, most / a.min_tiles));
+  return s >= 1 && (most + s - 1) / s <= T / a.n_cta + a.start_tiles ? s : 0;
+}
+
 // Where a CTA begins: entry e, tile `off` of its Hkv * span.n tiles, and the
-// CTA's range [x0, x1) (direct: of items).
+// CTA's range [x0, x1) (direct: of items).  even: entry e, head off, piece x0 of x1.
 struct PlanStart {
-  int e, off, x0, x1;
+  int e, off, x0, x1, even;
 };
 
 // Run by one whole warp; CTA 0 also writes the prefix table for the merge.
@@ -91,16 +105,19 @@ template <int LOGT>
 __device__ __forceinline__ PlanStart plan_start(const KvAttnArgs& a, int cta, int lane) {
   const int E = a.B * a.n_rt, Hkv = a.c.Hkv;
   PlanStart p;
+  p.even = 0;
   if (a.direct) {
     p.e = p.off = 0;
     p.x0 = range_start(E * Hkv, cta, a.n_cta);
     p.x1 = range_start(E * Hkv, cta + 1, a.n_cta);
     return p;
   }
-  int carry = 0, incl = 0, mine = 0;
+  int carry = 0, incl = 0, mine = 0, most = 0;
   for (int e0 = 0; e0 < E; e0 += 32) {
     const int e = e0 + lane;
-    mine = e < E ? entry_of<LOGT>(a, e).span.n * Hkv : 0;
+    mine = e < E ? entry_of<LOGT>(a, e).span.n : 0;
+    most = max(most, __reduce_max_sync(0xffffffffu, mine));
+    mine *= Hkv;
     incl = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -111,9 +128,23 @@ __device__ __forceinline__ PlanStart plan_start(const KvAttnArgs& a, int cta, in
     carry += __shfl_sync(0xffffffffu, incl, 31);
   }
   const int T = carry;
-  if (cta == 0 && lane == 0) a.prefix[E] = T;
-  p.x0 = range_start(T, cta, a.n_cta);
-  p.x1 = range_start(T, cta + 1, a.n_cta);
+  const int s = even_pieces(a, T, E * Hkv, most);
+  if (cta == 0 && lane == 0) {
+    a.prefix[E] = T;
+    a.prefix[E + 1] = s;
+  }
+  if (s > 0) {
+    const int item = cta / s;
+    p.even = 1;
+    p.e = item / Hkv;
+    p.off = item - p.e * Hkv;
+    p.x0 = cta - item * s;
+    p.x1 = s;
+    return p;
+  }
+  const int P = range_ctas(T, a);
+  p.x0 = range_start(T, min(cta, P), P);
+  p.x1 = range_start(T, min(cta + 1, P), P);
   p.e = 0;
   p.off = 0;
   if (p.x0 >= p.x1) return p;
@@ -143,7 +174,7 @@ __device__ __forceinline__ PlanStart plan_start(const KvAttnArgs& a, int cta, in
 
 // Walk over the CTA's segments: parts [u0, u1) of one item's tiles.
 struct SegWalk {
-  int e, off, x, x0, x1;
+  int e, off, x, x0, x1, even;
   Entry t;
   int hk, u0, u1;
   bool fresh;                       // t is entry e
@@ -152,6 +183,7 @@ struct SegWalk {
     off = p.off;
     x = x0 = p.x0;
     x1 = p.x1;
+    even = p.even;
     fresh = false;
   }
   template <int LOGT>
@@ -169,6 +201,15 @@ struct SegWalk {
       return false;
     }
     const int E = a.B * a.n_rt;
+    if (even) {
+      if (x >= x1 || e >= E) return false;
+      t = entry_of<LOGT>(a, e);
+      hk = off;
+      u0 = range_start(t.span.n, x, x1);
+      u1 = range_start(t.span.n, x + 1, x1);
+      x = x1;                       // one piece
+      return u1 > u0;
+    }
     while (x < x1 && e < E) {
       if (!fresh) {
         t = entry_of<LOGT>(a, e);
@@ -190,7 +231,7 @@ struct SegWalk {
     return false;
   }
   // the segment's place among the CTA's partials: 0 if it opens the range, else 1
-  __device__ __forceinline__ int slot() const { return x - (u1 - u0) == x0 ? 0 : 1; }
+  __device__ __forceinline__ int slot() const { return even || x - (u1 - u0) == x0 ? 0 : 1; }
   __device__ __forceinline__ bool whole() const { return u0 == 0 && u1 == t.span.n; }
 };
 

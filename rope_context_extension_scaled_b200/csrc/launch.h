@@ -80,13 +80,19 @@ int quantize_i8_launch(const QuantArgs& a, bool rows16, int grid, cudaStream_t s
 int kv_block_append_launch(const KvAppendArgs& a, int dtype, int kind, dim3 grid, int block, cudaStream_t stream);
 int kv_block_read_launch(const KvReadArgs& a, int dtype, int kind, dim3 grid, cudaStream_t stream);
 constexpr int kKvFewRows = 32;         // rows (tokens x heads of a group) up to which the mma.sync kernel runs
-constexpr int kKvFewTile = 32;         // its key tile and resident CTAs
-constexpr int kKvFewCtasPerSm = 2;
+constexpr int kKvFewTile = 32;         // its key tile
 constexpr int kKvFewWarps = 4;         // warps of its CTA, a tile each
-constexpr int kKvFewMergeTiles = 8;    // what a scan and a merge cost, in tile times (see kv_attn_impl)
+// resident CTAs and copy stages of the kernel for head dim D and nt columns of 8 rows
+constexpr int kv_few_ctas(int D, int nt) { return 2; }
+constexpr int kv_few_stages(int D, int nt) { return 3; }
+constexpr int kKvFewMinTiles = 4;      // tiles a CTA takes at least
+constexpr int kKvFewStartTiles = 24;   // beginning an item costs a CTA as much as so many tiles
+constexpr int kKvFewMergeTiles = 6;    // what a scan and a merge cost, in tile times (see kv_attn_impl)
 constexpr int kKvTcRows = 256;         // rows of an item of the tcgen05 kernel, and its key tile
 constexpr int kKvTcTile = 128;
-constexpr int kKvTcMergeTiles = 3;
+constexpr int kKvTcMinTiles = 3;
+constexpr int kKvTcStartTiles = 4;
+constexpr int kKvTcMergeTiles = 4;
 constexpr int kKvMaxSlice = 4096;      // sequences a launch takes
 constexpr int kKvReadPerCta = 512;     // 16-code pieces a CTA of the read kernel takes
 int attn_kv_block_launch_int8(const KvAttnArgs& a, cudaStream_t stream);

@@ -739,11 +739,11 @@ int kv_attn_plan(const rcx_tensor& q, const KvBlockView& c, int64_t B, KvAttnPla
   const int64_t tiles = (int64_t)c.Hkv * p->n_rt * (((int64_t)c.cap + tile - 1) / tile + 1);
   if (tiles > 0x7fffffff) return RCX_ERR_UNSUPPORTED;    // the kernels count tiles in 32 bits
   p->slice = std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(B, kKvMaxSlice), 0x7fffffff / tiles));
-  const int64_t ctas = (int64_t)sm_count() * (p->few ? kKvFewCtasPerSm : 1);
+  const int64_t ctas = (int64_t)sm_count() * (p->few ? kv_few_ctas((int)D, p->rows_item / 8) : 1);
   p->n_cta = (int)std::min<int64_t>(ctas, p->slice * tiles);
   p->off_lse = align256((int64_t)p->n_cta * 2 * p->rows_item * D * 4);
   p->off_prefix = align256(p->off_lse + (int64_t)p->n_cta * 2 * p->rows_item * 4);
-  p->total = align256(p->off_prefix + (p->slice * p->n_rt + 1) * 4);
+  p->total = align256(p->off_prefix + (p->slice * p->n_rt + 2) * 4);
   return RCX_OK;
 }
 
@@ -798,7 +798,9 @@ int kv_attn_impl(const rcx_tensor& q, const rcx_kv_blocks* cache, const int64_t*
   if (window > 0 && window < reach) reach = std::min<int64_t>(reach, window + rows_tok + a.n_sink + 2 * tile);
   const int64_t most = (reach + tile - 1) / tile;
   const int64_t lanes = p.few ? kKvFewWarps : 1;            // tiles a CTA works on at once
-  const int64_t ctas = (int64_t)sm_count() * (p.few ? kKvFewCtasPerSm : 1);
+  const int64_t ctas = (int64_t)sm_count() * (p.few ? kv_few_ctas((int)D, p.rows_item / 8) : 1);
+  a.min_tiles = p.few ? kKvFewMinTiles : kKvTcMinTiles;
+  a.start_tiles = p.few ? kKvFewStartTiles : kKvTcStartTiles;
   for (int64_t b0 = 0; b0 < B; b0 += p.slice) {
     a.b0 = (int)b0;
     a.B = (int)std::min<int64_t>(B - b0, p.slice);
