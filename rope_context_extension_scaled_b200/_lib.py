@@ -1,17 +1,19 @@
-"""ctypes binding of librcx.so (include/rcx.h): argument marshalling only.
+"""Binding of librcx.so (include/rcx.h): argument marshalling only.
 
 Every step of the computation runs in the library's CUDA kernels; this module
 turns torch tensors into rcx_tensor views (data pointer, dtype, shape,
 strides), passes the current CUDA stream, and maps status codes to
-exceptions.  PyTorch provides device memory and streams.  If the library is
-missing, load() raises: there is no fallback path.
+exceptions, through ctypes, or for the calls of a decoding step through the
+extension module _rcx_torch.  PyTorch provides device memory and streams.  If the
+library is missing, load() raises: there is no fallback path.
 """
 
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
-import struct
 
 import numpy as np
 import torch
@@ -432,62 +434,25 @@ def attn_decode_fwd(q, k, v, o=None, lse=None, window=0, n_sink=0, temperature=1
 # ------------------------------------------------- rotation by several axes
 #
 # The calls below serve decoding steps, whose kernels run for a few
-# microseconds: views are packed in one go, device and stream are read as
-# integers.
+# microseconds: their tensors are marshalled by _rcx_torch (csrc/torch_binding.cpp),
+# which also checks types and devices, instead of through ctypes.
 
-_DTYPES = {torch.float32: RCX_F32, torch.bfloat16: RCX_BF16, torch.int8: RCX_I8, torch.float8_e4m3fn: RCX_E4M3}
-_NULL = RcxTensor()
-_PACK = struct.Struct("Pi4x4q4q").pack                      # the layout of RcxTensor
-_PACK_LSE = struct.Struct("Pi4x3qq3qq").pack
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
-    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+EXT_PATH = os.path.join(_PKG, "_rcx_torch.so")
+_ext = None
 
 
-def _view4(t):
-    """view() of a tensor that the caller knows to be there."""
-    code = _DTYPES.get(t.dtype)
-    if code is None:
-        raise TypeError(f"unsupported dtype {t.dtype}")
-    if t.dim() != 4:
-        raise ValueError("expected a 4-D [B, N, H, d] tensor")
-    return RcxTensor.from_buffer_copy(_PACK(t.data_ptr(), code, *t.shape, *t.stride()))
-
-
-def _view3(t):
-    """lse_view() of a tensor that the caller knows to be there."""
-    if t.dim() != 3 or t.dtype != torch.float32:
-        raise ValueError("expected a 3-D [B, H, N] float32 tensor")
-    return RcxTensor.from_buffer_copy(_PACK_LSE(t.data_ptr(), RCX_F32, *t.shape, 1, *t.stride(), 1))
-
-
-def _one_device(first, *rest):
-    """Index of the CUDA device that all tensors (None: left out) are on."""
-    index = first.get_device()
-    if index < 0:
-        raise ValueError(f"expected CUDA tensors, got one on {first.device}")
-    for t in rest:
-        if t is not None and t.get_device() != index:
-            raise ValueError(f"tensors on different devices: {first.device} and {t.device}")
-    return index
-
-
-def _call(fn, index, *args):
-    """fn(*args, current stream of device `index`) with that device current."""
-    if index != torch.cuda.current_device():
-        with torch.cuda.device(index):
-            return fn(*args, _raw_stream(index))
-    return fn(*args, _raw_stream(index))
-
-
-def _per_sequence(t, name, B, index):
-    """Pointer of a contiguous int64 [B] tensor on the device (None: a null pointer)."""
-    if t is None:
-        return None
-    if t.dtype != torch.int64 or t.dim() != 1 or t.shape[0] != B or (B > 1 and t.stride(0) != 1):
-        raise ValueError(f"{name} must be a contiguous int64 [{B}] tensor")
-    if t.get_device() != index:
-        raise ValueError(f"{name} is on {t.device}, the other tensors on CUDA device {index}")
-    return t.data_ptr()
+def _fast():
+    """Load _rcx_torch.so (built in-tree beside librcx.so); raise if it is missing."""
+    global _ext
+    if _ext is None:
+        load()
+        if not os.path.exists(EXT_PATH):
+            raise RuntimeError(f"{EXT_PATH} is not built: run `python -m rope_context_extension_scaled_b200.build`")
+        loader = importlib.machinery.ExtensionFileLoader("_rcx_torch", EXT_PATH)
+        ext = importlib.util.module_from_spec(importlib.util.spec_from_loader("_rcx_torch", loader))
+        loader.exec_module(ext)
+        _ext = ext
+    return _ext
 
 
 def rope_axes_map(sections, interleaved=False):
@@ -513,24 +478,9 @@ def rope_axes_apply(q, k, inv_freq, axis, positions, halves=False, inverse=False
         return None, None
     q_out = q if q_out is None else q_out
     k_out = k if k_out is None else k_out
-    ref = q if q is not None else k
-    B, N, _, d = ref.shape
-    if positions.dtype != torch.int64 or positions.dim() != 3 or positions.shape[1] != B or positions.shape[2] != N:
-        raise ValueError(f"positions must be an int64 [axes, {B}, {N}] tensor")
-    sa, sb, sn = positions.stride()
-    if N > 1 and sn != 1:
-        raise ValueError("positions must have unit stride over tokens")
-    inv = np.asarray(inv_freq, dtype=np.float64)
-    ax = np.asarray(axis, dtype=np.int32)
-    if inv.shape != (d // 2,) or ax.shape != (d // 2,):
-        raise ValueError("inv_freq and axis need d/2 entries")
-    nq, nk = q is None, k is None
-    index = _one_device(ref, positions, k, None if nk else k_out, None if nq else q_out)
-    tq = _NULL if nq else _view4(q)
-    tk = _NULL if nk else _view4(k)
-    st = _call(load().rcx_rope_axes_apply, index, tq, tk, tq if nq or q_out is q else _view4(q_out),
-               tk if nk or k_out is k else _view4(k_out), positions.data_ptr(), positions.shape[0], sa, sb,
-               inv.tobytes(), ax.tobytes(), (ROPE_HALVES if halves else 0) | (ROPE_INVERSE if inverse else 0))
+    st = (_ext or _fast()).rope_axes_apply(q, k, q_out, k_out, np.asarray(inv_freq, np.float64),
+                                           np.asarray(axis, np.int32), positions,
+                                           (ROPE_HALVES if halves else 0) | (ROPE_INVERSE if inverse else 0))
     if st:
         _check(st, "rcx_rope_axes_apply")
     return q_out, k_out
@@ -556,20 +506,19 @@ class KvBlockCache:
                 raise ValueError(f"scales must be contiguous float32 [{n}, {h}] tensors")
         if table.dtype != torch.int32 or table.dim() != 2 or (table.shape[1] > 1 and table.stride(1) != 1):
             raise ValueError("table must be an int32 [B, width] tensor with unit stride over blocks")
-        self.index = _one_device(k, v, k_scale, v_scale, table)
+        for x in (k, v, k_scale, v_scale, table):
+            if not x.is_cuda or x.device != k.device:
+                raise ValueError(f"expected CUDA tensors on one device, got {k.device} and {x.device}")
         self.k, self.v, self.k_scale, self.v_scale, self.table = k, v, k_scale, v_scale, table
-        self.view = RcxKvBlocks(_view4(k), _view4(v), k_scale.data_ptr(), v_scale.data_ptr(), table.data_ptr(),
+        self.view = RcxKvBlocks(view(k), view(v), k_scale.data_ptr(), v_scale.data_ptr(), table.data_ptr(),
                                 table.shape[0], table.shape[1], table.stride(0))
-        self._ref = ctypes.byref(self.view)
+        self.address = ctypes.addressof(self.view)
 
 
 def kv_block_append(k, v, cache, start, count=None):
     """Quantise tokens start[b] .. start[b] + count[b] - 1 (rows of k, v [B, N, Hkv,
     d], bf16 or fp32; count None: N each) into the cache's blocks."""
-    index = _one_device(cache.k, k, v)
-    B = k.shape[0]
-    st = _call(load().rcx_kv_block_append, index, _view4(k), _view4(v), cache._ref,
-               _per_sequence(start, "start", B, index), _per_sequence(count, "count", B, index))
+    st = (_ext or _fast()).kv_block_append(k, v, cache.k, cache.address, start, count)
     if st:
         _check(st, "rcx_kv_block_append")
 
@@ -577,23 +526,17 @@ def kv_block_append(k, v, cache, start, count=None):
 def kv_block_read(cache, lengths, n, dtype=torch.bfloat16, k_out=None, v_out=None):
     """The first n tokens of each sequence as k, v [B, n, Hkv, d] in dtype (bf16 or
     fp32), zeros from token lengths[b] on."""
-    B, (_, _, H, d) = cache.table.shape[0], cache.k.shape
-    if k_out is None:
-        k_out = torch.empty(B, n, H, d, dtype=dtype, device=cache.k.device)
-    if v_out is None:
-        v_out = torch.empty(B, n, H, d, dtype=dtype, device=cache.k.device)
-    index = _one_device(cache.k, k_out, v_out)
-    if k_out.shape[1] != n:
-        raise ValueError(f"outputs must hold n = {n} tokens")
-    st = _call(load().rcx_kv_block_read, index, cache._ref, _per_sequence(lengths, "lengths", B, index),
-               _view4(k_out), _view4(v_out))
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"unsupported dtype {dtype}")
+    st, k_out, v_out = (_ext or _fast()).kv_block_read(cache.k, cache.address, cache.view.B, lengths, n, k_out, v_out,
+                                                       dtype == torch.bfloat16)
     if st:
         _check(st, "rcx_kv_block_read")
     return k_out, v_out
 
 
 def attn_kv_block_workspace_size(q, cache):
-    n = load().rcx_attn_kv_block_workspace_size(_view4(q), cache._ref)
+    n = load().rcx_attn_kv_block_workspace_size(view(q), ctypes.byref(cache.view))
     if n < 0:
         raise RcxError(RCX_ERR_INVALID_ARG, "rcx_attn_kv_block_workspace_size")
     return int(n)
@@ -606,17 +549,8 @@ def attn_kv_block_fwd(q, cache, start, count=None, o=None, lse=None, window=0, n
 
     Rows from count[b] on give O = 0, lse = -inf.  workspace: uint8 tensor of
     attn_kv_block_workspace_size(q, cache) bytes (None: a new one)."""
-    index = _one_device(cache.k, q, o, lse, workspace)
-    B, N, H, d = q.shape
-    if o is None:
-        o = torch.empty(B, N, H, d, dtype=q.dtype, device=q.device)
-    if lse is None and want_lse:
-        lse = torch.empty(B, H, N, dtype=torch.float32, device=q.device)
-    if workspace is None:
-        workspace = torch.empty(max(attn_kv_block_workspace_size(q, cache), 256), dtype=torch.uint8, device=q.device)
-    st = _call(load().rcx_attn_kv_block_fwd, index, _view4(q), cache._ref, _per_sequence(start, "start", B, index),
-               _per_sequence(count, "count", B, index), _view4(o), _NULL if lse is None else _view3(lse), int(window),
-               int(n_sink), float(temperature), workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    st, o, lse = (_ext or _fast()).attn_kv_block_fwd(q, cache.k, cache.address, start, count, o, lse, window, n_sink,
+                                                     temperature, workspace, want_lse)
     if st:
         _check(st, "rcx_attn_kv_block_fwd")
     return o, lse

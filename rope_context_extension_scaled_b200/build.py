@@ -4,7 +4,8 @@
 
 Each csrc/*.cu file is one translation unit (the C-ABI host code, and one
 unit per kernel family); they are compiled in parallel with nvcc and linked
-into one shared library.
+into one shared library.  csrc/torch_binding.cpp becomes the extension module
+_rcx_torch.so, which links to it and to the installed torch.
 """
 
 from __future__ import annotations
@@ -18,6 +19,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OBJ = os.path.join(PKG, "_build")
 OUT = os.path.join(PKG, "librcx.so")
+EXT_SRC = os.path.join(CSRC, "torch_binding.cpp")
+EXT = os.path.join(PKG, "_rcx_torch.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = [
@@ -33,7 +36,7 @@ def units():
 
 
 def headers():
-    return [os.path.join(CSRC, f) for f in sorted(os.listdir(CSRC)) if not f.endswith(".cu")] + \
+    return [os.path.join(CSRC, f) for f in sorted(os.listdir(CSRC)) if not f.endswith((".cu", ".cpp"))] + \
         [os.path.join(ROOT, "include", "rcx.h")]
 
 
@@ -51,8 +54,31 @@ def up_to_date() -> bool:
     return _newest(units() + headers() + [os.path.abspath(__file__)]) <= os.path.getmtime(OUT)
 
 
+def build_ext(force: bool = False) -> str:
+    """Compile _rcx_torch.so against the installed torch (librcx.so has to be there)."""
+    deps = [EXT_SRC, os.path.join(ROOT, "include", "rcx.h"), os.path.abspath(__file__)]
+    if not force and os.path.exists(EXT) and _newest(deps) <= os.path.getmtime(EXT):
+        return EXT
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")]
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-o", EXT + ".tmp",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-I{p}" for p in inc), EXT_SRC,
+           "-L" + PKG, "-l:librcx.so", "-Wl,-rpath,$ORIGIN", "-L" + os.path.join(root, "lib"), "-ltorch_python",
+           "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("torch_binding.cpp failed:\n" + r.stdout + r.stderr)
+    os.replace(EXT + ".tmp", EXT)
+    return EXT
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     if not force and up_to_date():
+        build_ext()
         return OUT
     nvcc = os.environ.get("NVCC", "nvcc")
     os.makedirs(OBJ, exist_ok=True)
@@ -82,6 +108,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError("nvcc link failed:\n" + r.stdout + r.stderr)
     os.replace(OUT + ".tmp", OUT)
+    build_ext(force)
     return OUT
 
 
