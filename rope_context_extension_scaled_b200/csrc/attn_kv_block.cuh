@@ -83,7 +83,6 @@ __global__ void __launch_bounds__(kKbWarps * 32, kv_few_ctas(D, NT)) attn_kv_blo
     const PlanStart p = plan_start<LOGT>(a, blockIdx.x, lane);
     if (lane == 0) sm_plan = p;
   }
-  if (a.direct) empty_rows<D>(a, warp, kKbWarps, lane);
   __syncthreads();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   SegWalk w;
@@ -103,6 +102,70 @@ __global__ void __launch_bounds__(kKbWarps * 32, kv_few_ctas(D, NT)) attn_kv_blo
   while (w.next<LOGT>(a)) {
     const Entry& t = w.t;
     const int64_t b = t.b;
+    // ---- this warp's tiles: u0 + warp, u0 + warp + kKbWarps, ...
+    const int ub = w.u0 + warp;
+    const int nk = ub < w.u1 ? (w.u1 - ub + kKbWarps - 1) / kKbWarps : 0;
+    const KeySpan span = t.span;
+    const int hi = span.hi;
+    const int32_t* trow = kv.table + b * kv.t_sb;
+    const float* ksh = kv.ks + w.hk;
+    const float* vsh = kv.vs + w.hk;
+    auto load_meta = [&](int batch, int& ph, float& ks, float& vs) {
+      ph = 0;
+      ks = vs = 0.f;
+      const int kk = 16 * batch + (lane >> 1);
+      if (kk < nk) {
+        const int key = (span.tile(ub + kKbWarps * kk) << LOGT) + ((lane & 1) << 4);
+        if (key < hi) {
+          int e = trow[key >> lb];
+          if ((unsigned)e >= (unsigned)kv.n_blocks) {
+            record_device_error(RCX_ERR_DEVICE_INDEX);
+            e = 0;
+          }
+          ph = e;
+          ks = ksh[(int64_t)e * kv.Hkv];
+          vs = vsh[(int64_t)e * kv.Hkv];
+          if (!(fabsf(vs) < INFINITY)) vs = __uint_as_float(0x7fffffffu);
+        }
+      }
+    };
+    const uint8_t* kb = kv.k + w.hk * kv.k_sh + cp * 16;
+    const uint8_t* vb = kv.v + w.hk * kv.v_sh + cp * 16;
+    int ph_a, ph_b = 0;
+    float ks_a, vs_a, ks_b, vs_b;
+    load_meta(0, ph_a, ks_a, vs_a);
+    auto issue = [&](int kk, int batch, int st) {
+      if (kk < nk) {
+        const int src = (kk >> 4) == batch ? ph_a : ph_b;
+        const int key0 = span.tile(ub + kKbWarps * kk) << LOGT;
+        const int rem = hi - key0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int ph = __shfl_sync(0xffffffffu, src, 2 * (kk & 15) + h);
+          const int64_t tok = ((key0 + 16 * h) & bmask) + cr;
+          const uint8_t* kp = kb + ph * kv.k_sb + tok * kv.k_sn;
+          const uint8_t* vp = vb + ph * kv.v_sb + tok * kv.v_sn;
+#pragma unroll
+          for (int i = 0; i < 16 / kRowsPerCopy; ++i) {
+            const int r = 16 * h + cr + kRowsPerCopy * i;
+            const uint32_t dst = wbuf + st * kStage + r * D + ((cp ^ kb_swz<D>(r & 7)) * 16);
+            const int bytes = r < rem ? 16 : 0;   // rows behind the keys: zeros, nothing read
+            const int64_t step = bytes ? (int64_t)kRowsPerCopy * i : -(int64_t)cr;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(kp + step * kv.k_sn), "r"(bytes)
+                         : "memory");
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + kTile), "l"(vp + step * kv.v_sn),
+                         "r"(bytes)
+                         : "memory");
+          }
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int s = 0; s < kKbStages - 1; ++s) issue(s, 0, s);
+    load_meta(1, ph_b, ks_b, vs_b);
+
+    // the first tiles are on their way; now the queries
     // ---- Q^T operand: chunk i of lane (g, c) holds dims base + {0, 2}, base + {1, 3}
     // of row 8 nt + g, base = 16 c + 4 i (i < 4) or 64 + 16 c + 4 (i - 4)
     for (int nt = warp; nt < NT; nt += kKbWarps) {
@@ -165,69 +228,6 @@ __global__ void __launch_bounds__(kKbWarps * 32, kv_few_ctas(D, NT)) attn_kv_blo
         for (int e = 0; e < 4; ++e) o[mt][nt][e] = 0.f;
     float vref = 0.f;                            // largest V scale met so far
 
-    // ---- this warp's tiles: u0 + warp, u0 + warp + kKbWarps, ...
-    const int ub = w.u0 + warp;
-    const int nk = ub < w.u1 ? (w.u1 - ub + kKbWarps - 1) / kKbWarps : 0;
-    const KeySpan span = t.span;
-    const int hi = span.hi;
-    const int32_t* trow = kv.table + b * kv.t_sb;
-    const float* ksh = kv.ks + w.hk;
-    const float* vsh = kv.vs + w.hk;
-    auto load_meta = [&](int batch, int& ph, float& ks, float& vs) {
-      ph = 0;
-      ks = vs = 0.f;
-      const int kk = 16 * batch + (lane >> 1);
-      if (kk < nk) {
-        const int key = (span.tile(ub + kKbWarps * kk) << LOGT) + ((lane & 1) << 4);
-        if (key < hi) {
-          int e = trow[key >> lb];
-          if ((unsigned)e >= (unsigned)kv.n_blocks) {
-            record_device_error(RCX_ERR_DEVICE_INDEX);
-            e = 0;
-          }
-          ph = e;
-          ks = ksh[(int64_t)e * kv.Hkv];
-          vs = vsh[(int64_t)e * kv.Hkv];
-          if (!(fabsf(vs) < INFINITY)) vs = __uint_as_float(0x7fffffffu);
-        }
-      }
-    };
-    const uint8_t* kb = kv.k + w.hk * kv.k_sh + cp * 16;
-    const uint8_t* vb = kv.v + w.hk * kv.v_sh + cp * 16;
-    int ph_a, ph_b;
-    float ks_a, vs_a, ks_b, vs_b;
-    load_meta(0, ph_a, ks_a, vs_a);
-    load_meta(1, ph_b, ks_b, vs_b);
-    auto issue = [&](int kk, int batch, int st) {
-      if (kk < nk) {
-        const int src = (kk >> 4) == batch ? ph_a : ph_b;
-        const int key0 = span.tile(ub + kKbWarps * kk) << LOGT;
-        const int rem = hi - key0;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int ph = __shfl_sync(0xffffffffu, src, 2 * (kk & 15) + h);
-          const int64_t tok = ((key0 + 16 * h) & bmask) + cr;
-          const uint8_t* kp = kb + ph * kv.k_sb + tok * kv.k_sn;
-          const uint8_t* vp = vb + ph * kv.v_sb + tok * kv.v_sn;
-#pragma unroll
-          for (int i = 0; i < 16 / kRowsPerCopy; ++i) {
-            const int r = 16 * h + cr + kRowsPerCopy * i;
-            const uint32_t dst = wbuf + st * kStage + r * D + ((cp ^ kb_swz<D>(r & 7)) * 16);
-            const int bytes = r < rem ? 16 : 0;   // rows behind the keys: zeros, nothing read
-            const int64_t step = bytes ? (int64_t)kRowsPerCopy * i : -(int64_t)cr;
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(kp + step * kv.k_sn), "r"(bytes)
-                         : "memory");
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + kTile), "l"(vp + step * kv.v_sn),
-                         "r"(bytes)
-                         : "memory");
-          }
-        }
-      }
-      asm volatile("cp.async.commit_group;" ::: "memory");
-    };
-#pragma unroll
-    for (int s = 0; s < kKbStages - 1; ++s) issue(s, 0, s);
-
     int st = 0;
     for (int kk = 0; kk < nk; ++kk) {
       const int batch = kk >> 4;
@@ -256,6 +256,11 @@ __global__ void __launch_bounds__(kKbWarps * 32, kv_few_ctas(D, NT)) attn_kv_blo
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[u][nt][e] = 0.f;
+        float s2[NT <= 2 ? NT : 1][4];           // a second chain halves the latency of the dot products
+#pragma unroll
+        for (int nt = 0; nt < (NT <= 2 ? NT : 1); ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s2[nt][e] = 0.f;
         uint32_t kw[2][kChunks];
 #pragma unroll
         for (int r = 0; r < 2; ++r)
@@ -272,8 +277,14 @@ __global__ void __launch_bounds__(kKbWarps * 32, kv_few_ctas(D, NT)) attn_kv_blo
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             const uint2 q = kQRegs ? qf[kQRegs ? nt : 0][i] : sm_q[(nt * kChunks + i) * 32 + lane];
-            mma_f16_16816(s[u][nt], af, q.x, q.y);
+            mma_f16_16816(NT <= 2 && (i & 1) ? s2[NT <= 2 ? nt : 0] : s[u][nt], af, q.x, q.y);
           }
+        }
+        if constexpr (NT <= 2) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[u][nt][e] += s2[nt][e];
         }
       }
       // logits in log2 units; a tile cut by the mask or the keys' end element by element
@@ -433,6 +444,7 @@ __global__ void __launch_bounds__(kKbWarps * 32, kv_few_ctas(D, NT)) attn_kv_blo
     }
     __syncthreads();                             // the buffers are free for the next segment
   }
+  if (a.direct) empty_rows<D>(a, warp, kKbWarps, lane);
 }
 
 // Merge of items that several CTAs share, by the LSE rule of rcx_merge_partials,
