@@ -1,5 +1,5 @@
-// Attention of a few query rows (one token, or a few drafted tokens, of each
-// sequence) over a block-scaled 8-bit paged KV cache, and the merge of partials.
+// Attention of few query rows (one token, or some drafted tokens, of each
+// sequence; items of at most 32 rows) over a block-scaled 8-bit paged KV cache, and the merge of partials.
 //
 // Key j of KV head h stands for k_code[j] * k_scale[block(j), h] (and likewise
 // V).  For every row:  x_j = (q . k_code_j) * k_scale * log2(e) / (sqrt(d) t),
@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(kKbWarps * 32, kv_few_ctas(D, NT)) attn_kv_blo
       float x[4 * kChunks];
       uint32_t mx = 0;
       if (r < t.rows) {
-        const int n = r / a.G, h = r - n * a.G;
+        const int n = (t.r0 + r) / a.G, h = t.r0 + r - n * a.G;
         const __nv_bfloat16* qp = static_cast<const __nv_bfloat16*>(a.q.ptr) + b * a.q.sb + (int64_t)n * a.q.sn +
                                   (int64_t)(w.hk * a.G + h) * a.q.sh + 16 * c;
 #pragma unroll
@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(kKbWarps * 32, kv_few_ctas(D, NT)) attn_kv_blo
       for (int h = 0; h < 2; ++h) {
         const int r = 8 * nt + 2 * c + h;
         fac[nt][h] = sm_fac[r];
-        qi[nt][h] = r < t.rows ? t.start + r / a.G : -1;
+        qi[nt][h] = r < t.rows ? t.start + (t.r0 + r) / a.G : -1;
         m[nt][h] = -INFINITY;
         l[nt][h] = 0.f;
       }
@@ -434,7 +434,7 @@ __global__ void __launch_bounds__(kKbWarps * 32, kv_few_ctas(D, NT)) attn_kv_blo
       ot.x *= inv; ot.y *= inv; ot.z *= inv; ot.w *= inv;
       const float lse = lt == 0.f ? -INFINITY : (mr - kKbUp + log2f(lt)) * 0.69314718055994530942f;
       if (whole) {
-        const int n = r / a.G, hq = w.hk * a.G + r - n * a.G;
+        const int n = (t.r0 + r) / a.G, hq = w.hk * a.G + t.r0 + r - n * a.G;
         store_o4(a, b * a.o.sb + (int64_t)n * a.o.sn + (int64_t)hq * a.o.sh + dd, ot);
         if (dd == 0 && a.lse) a.lse[b * a.lse_sb + hq * a.lse_sh + n] = lse;
       } else {

@@ -139,6 +139,19 @@ __device__ __forceinline__ void add2(float& a, float& b, float c, float d) {
       : "f"(c), "f"(d));
 }
 
+// A warp's arrival for what its lanes stored to shared memory for the MMAs.
+__device__ __forceinline__ void warp_arrive_stored(uint32_t bar, int lane) {
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+}
+
+// 32 bytes to global memory at once: a row's sectors are written whole although
+// every lane writes a row of its own.
+__device__ __forceinline__ void store_32b(void* p, const uint32_t* r) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), RCX_W8(0) : "memory");
+}
+
 template <int R>
 __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
 template <int R>
@@ -155,17 +168,17 @@ __global__ void __launch_bounds__(kBtThreads, 1) attn_kv_block_tc_kernel(const _
   const uint32_t bar0 = sbase + L::bar;
   auto BAR = [&](int i) { return bar0 + 8u * (uint32_t)i; };
   enum {
-    B_QREADY = 0,                     // [2] Q rows of the slot stored (128 arrivals)
-    B_KFULL = 2,                      // [stages] (128 arrivals)
+    B_QREADY = 0,                     // [2] Q rows of the slot stored (one arrival a warp)
+    B_KFULL = 2,                      // [stages] (one arrival a warp)
     B_KEMPTY = B_KFULL + kBtStages,
     B_VFULL = B_KEMPTY + kBtStages,
     B_VEMPTY = B_VFULL + kBtStages,
     B_SFULL = B_VEMPTY + kBtStages,   // [2]
-    B_PREADY = B_SFULL + 2,           // [2] (128 arrivals)
+    B_PREADY = B_SFULL + 2,           // [2] (one arrival a warp)
     B_OFINAL = B_PREADY + 2,          // [2]
-    B_META = B_OFINAL + 2,            // [ring] scales of a tile written (32 arrivals)
+    B_META = B_OFINAL + 2,            // [ring] scales of a tile written
     B_RFULL = B_META + kBtMeta,       // [K, V] codes of a tile landed
-    B_REMPTY = B_RFULL + 2,           // [K, V] they have been read (128 arrivals)
+    B_REMPTY = B_RFULL + 2,           // [K, V] they have been read (one arrival a warp)
     B_DRAIN = B_REMPTY + 2,
     B_NEVER,
     B_COUNT
@@ -183,8 +196,7 @@ __global__ void __launch_bounds__(kBtThreads, 1) attn_kv_block_tc_kernel(const _
       uint32_t cnt = 1;
       if (i < 2 || (i >= B_KFULL && i < B_KFULL + kBtStages) || (i >= B_VFULL && i < B_VFULL + kBtStages) ||
           i == B_PREADY || i == B_PREADY + 1 || i == B_REMPTY || i == B_REMPTY + 1)
-        cnt = 128;
-      if (i >= B_META && i < B_META + kBtMeta) cnt = 32;
+        cnt = 4;
       mbar_init(BAR(i), cnt);
     }
     *abort_flag = 0;
@@ -376,8 +388,8 @@ __global__ void __launch_bounds__(kBtThreads, 1) attn_kv_block_tc_kernel(const _
           mt->vref = vnew;
         }
         vref = vnew;
-        mbar_arrive(BAR(B_META + jg % kBtMeta));
         __syncwarp();
+        if (lane == 0) mbar_arrive(BAR(B_META + jg % kBtMeta));
         if (!(ok = warp_wait(B_REMPTY + 1, (jg & 1) ^ 1))) break;
         copy_codes(u, ph, 1);                     // its arrival also publishes the ratios
         ph = ph_next;
@@ -436,14 +448,12 @@ __global__ void __launch_bounds__(kBtThreads, 1) attn_kv_block_tc_kernel(const _
         const uint32_t par = ((jg / kBtStages) & 1) ^ 1;
         if (!(ok = warp_wait(B_KEMPTY + st, par) && warp_wait(B_RFULL, jg & 1))) break;
         store_tile(L::k + st * L::tile, raw_k, nullptr, std::false_type{});
-        fence_proxy_async_smem();
-        mbar_arrive(BAR(B_KFULL + st));
-        mbar_arrive(BAR(B_REMPTY));
+        warp_arrive_stored(BAR(B_KFULL + st), lane);
+        if (lane == 0) mbar_arrive(BAR(B_REMPTY));
         if (!(ok = warp_wait(B_VEMPTY + st, par) && warp_wait(B_RFULL + 1, jg & 1))) break;
         store_tile(L::v + st * L::tile, raw_v, meta[jg % kBtMeta].ratio, std::true_type{});
-        fence_proxy_async_smem();
-        mbar_arrive(BAR(B_VFULL + st));
-        mbar_arrive(BAR(B_REMPTY + 1));
+        warp_arrive_stored(BAR(B_VFULL + st), lane);
+        if (lane == 0) mbar_arrive(BAR(B_REMPTY + 1));
       }
     }
   } else {
@@ -454,49 +464,93 @@ __global__ void __launch_bounds__(kBtThreads, 1) attn_kv_block_tc_kernel(const _
     const int r = q4 * 32 + lane;               // row within the slot
     const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
     int jg = 0, js = 0, segs = 0;
-    while (ok && bt_next(w, a, lane)) {
-      const int n = w->n;
-      if (s * kBtM >= w->rows) {
-        jg += n;
-        continue;
+    // the slot's row of this thread in the current segment
+    int gi = 0, full_hi = 0, full_lo = 0;
+    float fac = 0.f;
+    // what the epilogue of the segment before needs
+    bool pending = false, whole = false, row_ok = false;
+    float inv = 0.f;
+    int64_t prow = 0, off = 0;
+    auto row_of = [&]() { return w->r0 + min(s * kBtM + r, w->rows - 1); };   // rows behind the last repeat it
+    // next segment with rows of this slot, and its Q rows: power-of-two scaled fp16
+    // in shared memory.  The buffer is free: the slot's last OFINAL came after every
+    // S MMA that read it.
+    auto next_rows = [&]() {
+      bool have = bt_next(w, a, lane);
+      while (have && s * kBtM >= w->rows) {
+        jg += w->n;
+        have = bt_next(w, a, lane);
       }
-      const bool row_ok = s * kBtM + r < w->rows;
-      const int rr = w->r0 + min(s * kBtM + r, w->rows - 1);   // rows behind the last repeat it
-      const int tok = rr / a.G, hq = w->hk * a.G + rr - tok * a.G;
-      const int gi = w->start + tok;
-      // ---- Q row -> power-of-two scaled fp16 in shared memory.  The buffer is free:
-      // the slot's last OFINAL came after every S MMA that read it.
-      float fac;
-      {
-        const uint4* qp = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q.ptr) + (int64_t)w->b * a.q.sb +
-                                                         (int64_t)tok * a.q.sn + (int64_t)hq * a.q.sh);
-        uint4 x[D / 8];
-        uint32_t mx = 0;
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) x[i] = qp[i];
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          const uint32_t wv[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) mx = max(mx, max(wv[e] & 0x7fff0000u, (wv[e] << 16) & 0x7fff0000u));
-        }
-        float up, down;
-        row_pow2(mx, up, down);
-        fac = down * a.scale_log2 * (KIND == 1 ? kE4m3Unscale : 1.f);
-        uint8_t* qrow = smem + L::q + s * L::tile + r * 128;
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          const float2 f0 = bf2_to_f2(x[i].x), f1 = bf2_to_f2(x[i].y), f2 = bf2_to_f2(x[i].z), f3 = bf2_to_f2(x[i].w);
-          const uint4 h = make_uint4(f2_to_h2(f0.x * up, f1.x * up), f2_to_h2(f0.y * up, f1.y * up),
-                                     f2_to_h2(f2.x * up, f3.x * up), f2_to_h2(f2.y * up, f3.y * up));
-          *reinterpret_cast<uint4*>(qrow + (i >> 3) * kBtHalf + (((i & 7) ^ (r & 7)) * 16)) = h;
-        }
-        fence_proxy_async_smem();
-        mbar_arrive(BAR(B_QREADY + s));
-      }
+      if (!have) return false;
+      const int rr = row_of(), tok = rr / a.G, hq = w->hk * a.G + rr - tok * a.G;
+      gi = w->start + tok;
       // tiles of keys full_lo < key0 <= full_hi, and sink tiles, need no mask for the slot's rows
-      const int full_hi = w->start + (w->r0 + s * kBtM) / a.G + 1 - kBtN;
-      const int full_lo = a.window == 0 ? -1 : w->start + (w->r0 + min((s + 1) * kBtM, w->rows) - 1) / a.G - a.window;
+      full_hi = w->start + (w->r0 + s * kBtM) / a.G + 1 - kBtN;
+      full_lo = a.window == 0 ? -1 : w->start + (w->r0 + min((s + 1) * kBtM, w->rows) - 1) / a.G - a.window;
+      const uint4* qp = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q.ptr) + (int64_t)w->b * a.q.sb +
+                                                       (int64_t)tok * a.q.sn + (int64_t)hq * a.q.sh);
+      uint4 x[D / 8];
+      uint32_t mx = 0;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) x[i] = qp[i];
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        const uint32_t wv[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mx = max(mx, max(wv[e] & 0x7fff0000u, (wv[e] << 16) & 0x7fff0000u));
+      }
+      float up, down;
+      row_pow2(mx, up, down);
+      fac = down * a.scale_log2 * (KIND == 1 ? kE4m3Unscale : 1.f);
+      uint8_t* qrow = smem + L::q + s * L::tile + r * 128;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        const float2 f0 = bf2_to_f2(x[i].x), f1 = bf2_to_f2(x[i].y), f2 = bf2_to_f2(x[i].z), f3 = bf2_to_f2(x[i].w);
+        const uint4 h = make_uint4(f2_to_h2(f0.x * up, f1.x * up), f2_to_h2(f0.y * up, f1.y * up),
+                                   f2_to_h2(f2.x * up, f3.x * up), f2_to_h2(f2.y * up, f3.y * up));
+        *reinterpret_cast<uint4*>(qrow + (i >> 3) * kBtHalf + (((i & 7) ^ (r & 7)) * 16)) = h;
+      }
+      warp_arrive_stored(BAR(B_QREADY + s), lane);
+      return true;
+    };
+    while (ok) {
+      const bool have = next_rows();            // its first S MMAs run beside the stores below
+      if (pending) {
+#pragma unroll 1
+        for (int cb = 0; cb < D / 32; ++cb) {
+          uint32_t o[32];
+          tmem_ld32(tO(s) + lane_off + cb * 32, o);
+          tmem_wait_ld();
+          if (row_ok) {
+            float y[32];
+#pragma unroll
+            for (int c = 0; c < 32; c += 4) {     // columns hold dims 0, 2, 1, 3 of each four
+              y[c] = __uint_as_float(o[c]) * inv;
+              y[c + 1] = __uint_as_float(o[c + 2]) * inv;
+              y[c + 2] = __uint_as_float(o[c + 1]) * inv;
+              y[c + 3] = __uint_as_float(o[c + 3]) * inv;
+            }
+            if (!whole) {
+#pragma unroll
+              for (int c = 0; c < 32; c += 8) store_32b(a.part_o + prow * D + 32 * cb + c, reinterpret_cast<uint32_t*>(y) + c);
+            } else if (a.o_bf16 && a.o_wide) {
+              uint32_t h[16];
+#pragma unroll
+              for (int c = 0; c < 16; ++c) h[c] = f2_to_bf2(y[2 * c], y[2 * c + 1]);
+              __nv_bfloat16* op = static_cast<__nv_bfloat16*>(a.o.ptr) + off + 32 * cb;
+              store_32b(op, h);
+              store_32b(op + 16, h + 8);
+            } else {
+#pragma unroll
+              for (int c = 0; c < 32; c += 4) store_o4(a, off + 32 * cb + c, make_float4(y[c], y[c + 1], y[c + 2], y[c + 3]));
+            }
+          }
+        }
+        tc_fence_before();                      // O is read before the slot's next weights are announced
+        pending = false;
+      }
+      if (!have) break;
+      const int n = w->n;
       float m_used = -INFINITY, l = 0.f, vref = 0.f, poison = 0.f;
       for (int j = 0; j < n; ++j) {
         const int g = jg + j;
@@ -587,41 +641,29 @@ __global__ void __launch_bounds__(kBtThreads, 1) attn_kv_block_tc_kernel(const _
         }
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(BAR(B_PREADY + s));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(BAR(B_PREADY + s));
       }
       if (!ok) break;
 
       // ---- epilogue: O / l -> the output row, or a partial for the merge
       if (!(ok = __all_sync(0xffffffffu, mbar_wait(BAR(B_OFINAL + s), segs & 1, abort_flag)))) break;
       tc_fence_after();
-      const bool whole = w->whole;
+      const int rr = row_of(), tok = rr / a.G, hq = w->hk * a.G + rr - tok * a.G;
+      whole = w->whole;
+      row_ok = s * kBtM + r < w->rows;
       const float lse = l == 0.f ? -INFINITY : (m_used - kKbUp + log2f(l)) * 0.69314718055994530942f;
-      const float inv = (l == 0.f ? 0.f : vref * ((KIND == 1 ? kE4m3Unscale : 1.f) / kBtVUp<KIND>) / l) + poison;
-      const int64_t prow = ((int64_t)blockIdx.x * 2 + w->slot) * a.rows_item + s * kBtM + r;
-      const int64_t off = (int64_t)w->b * a.o.sb + (int64_t)tok * a.o.sn + (int64_t)hq * a.o.sh;
-#pragma unroll 1
-      for (int cb = 0; cb < D / 32; ++cb) {
-        uint32_t o[32];
-        tmem_ld32(tO(s) + lane_off + cb * 32, o);
-        tmem_wait_ld();
-        if (row_ok) {
-#pragma unroll
-          for (int c = 0; c < 32; c += 4) {     // columns hold dims 0, 2, 1, 3 of each four
-            const float4 y = make_float4(__uint_as_float(o[c]) * inv, __uint_as_float(o[c + 2]) * inv,
-                                         __uint_as_float(o[c + 1]) * inv, __uint_as_float(o[c + 3]) * inv);
-            if (whole) store_o4(a, off + 32 * cb + c, y);
-            else *reinterpret_cast<float4*>(a.part_o + prow * D + 32 * cb + c) = y;
-          }
-        }
-      }
+      inv = (l == 0.f ? 0.f : vref * ((KIND == 1 ? kE4m3Unscale : 1.f) / kBtVUp<KIND>) / l) + poison;
+      prow = ((int64_t)blockIdx.x * 2 + w->slot) * a.rows_item + s * kBtM + r;
+      off = (int64_t)w->b * a.o.sb + (int64_t)tok * a.o.sn + (int64_t)hq * a.o.sh;
       if (row_ok) {
         if (!whole) a.part_lse[prow] = lse;
         else if (a.lse) a.lse[(int64_t)w->b * a.lse_sb + hq * a.lse_sh + tok] = lse;
       }
-      tc_fence_before();                        // O is read before the next segment's MMAs write it (QREADY orders)
       jg += n;
       js += n;
       ++segs;
+      pending = true;
     }
   }
 

@@ -41,6 +41,7 @@ struct KvAttnArgs {
   int window, n_sink;               // window 0 = none
   float scale_log2;                 // log2(e) / (sqrt(d) * t)
   int o_bf16;
+  int o_wide;                       // rows of o are 32-byte aligned
   int rows_item;                    // rows (token, head of the group) an item holds
   int n_rt;                         // items a (sequence, KV head) has at most
   int n_cta;                        // CTAs the key tiles (direct: items) are dealt to

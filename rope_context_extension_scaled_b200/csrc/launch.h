@@ -79,7 +79,8 @@ int quantize_i8_launch(const QuantArgs& a, bool rows16, int grid, cudaStream_t s
 // ---- k_kv_block.cu, k_attn_kv_block_*.cu (kind: 0 int8, 1 e4m3 codes)
 int kv_block_append_launch(const KvAppendArgs& a, int dtype, int kind, dim3 grid, int block, cudaStream_t stream);
 int kv_block_read_launch(const KvReadArgs& a, int dtype, int kind, dim3 grid, cudaStream_t stream);
-constexpr int kKvFewRows = 32;         // rows (tokens x heads of a group) up to which the mma.sync kernel runs
+constexpr int kKvFewRows = 64;         // rows (tokens x heads of a group) up to which the mma.sync kernel runs
+constexpr int kKvFewItemRows = 32;     // rows of an item of it, at most
 constexpr int kKvFewTile = 32;         // its key tile
 constexpr int kKvFewWarps = 4;         // warps of its CTA, a tile each
 // resident CTAs and copy stages of the kernel for head dim D and nt columns of 8 rows

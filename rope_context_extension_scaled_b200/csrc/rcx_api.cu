@@ -732,8 +732,11 @@ int kv_attn_plan(const rcx_tensor& q, const KvBlockView& c, int64_t B, KvAttnPla
   if (G > 65535 || N > 0x3fffffff / G) return RCX_ERR_UNSUPPORTED;
   const int64_t rows = N * G;
   p->few = rows <= kKvFewRows;
-  p->rows_item = p->few ? (int)((rows + 7) / 8 * 8) : kKvTcRows;
-  p->n_rt = p->few ? 1 : (int)((rows + kKvTcRows - 1) / kKvTcRows);
+  // few rows: items of equal size, at most 32 rows, in eights
+  const int64_t most_rows = p->few ? kKvFewItemRows : kKvTcRows;
+  p->n_rt = (int)std::max<int64_t>(1, (rows + most_rows - 1) / most_rows);
+  p->rows_item = p->few ? (int)((rows + 8 * p->n_rt - 1) / (8 * p->n_rt) * 8) : kKvTcRows;
+  if (p->few) p->n_rt = (int)std::max<int64_t>(1, (rows + p->rows_item - 1) / std::max(1, p->rows_item));
   const int64_t tile = p->few ? kKvFewTile : kKvTcTile;
   // key tiles of one sequence: all its items', sinks' partial tile included
   const int64_t tiles = (int64_t)c.Hkv * p->n_rt * (((int64_t)c.cap + tile - 1) / tile + 1);
@@ -773,6 +776,7 @@ int kv_attn_impl(const rcx_tensor& q, const rcx_kv_blocks* cache, const int64_t*
   a.q = make_view(q);
   a.o = make_view(o);
   a.o_bf16 = o.dtype == RCX_BF16;
+  a.o_wide = aligned_rows(o, 32);
   a.lse = static_cast<float*>(lse.ptr);
   a.lse_sb = lse.ptr ? lse.stride[0] : 0;
   a.lse_sh = lse.ptr ? lse.stride[1] : 0;
@@ -793,7 +797,7 @@ int kv_attn_impl(const rcx_tensor& q, const rcx_kv_blocks* cache, const int64_t*
   a.inject_spins = p.few ? 0 : attn_tc_inject();
   // Most key tiles an item can have: all its rows' windows and the sinks.
   const int64_t tile = p.few ? kKvFewTile : kKvTcTile;
-  const int64_t rows_tok = p.few ? N : std::min<int64_t>(N, kKvTcRows / a.G + 2);
+  const int64_t rows_tok = std::min<int64_t>(N, p.rows_item / a.G + 2);
   int64_t reach = a.c.cap;
   if (window > 0 && window < reach) reach = std::min<int64_t>(reach, window + rows_tok + a.n_sink + 2 * tile);
   const int64_t most = (reach + tile - 1) / tile;
