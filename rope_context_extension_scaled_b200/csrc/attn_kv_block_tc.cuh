@@ -146,12 +146,6 @@ __device__ __forceinline__ void warp_arrive_stored(uint32_t bar, int lane) {
   if (lane == 0) mbar_arrive(bar);
 }
 
-// 32 bytes to global memory at once: a row's sectors are written whole although
-// every lane writes a row of its own.
-__device__ __forceinline__ void store_32b(void* p, const uint32_t* r) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), RCX_W8(0) : "memory");
-}
-
 template <int R>
 __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
 template <int R>

@@ -143,9 +143,10 @@ static __global__ void __launch_bounds__(512) kv_block_append_kernel(const KvApp
   __shared__ uint32_t sm_max[16];
   const KvBlockView& c = a.c;
   const int tid = threadIdx.x, nt = blockDim.x;
-  const int hk = blockIdx.y >> 1, isv = blockIdx.y & 1, b = blockIdx.z + a.b0;
+  const unsigned g = blockIdx.x / (unsigned)c.Hkv, hk = blockIdx.x - g * (unsigned)c.Hkv;
+  const int isv = g & 1, b = blockIdx.y + a.b0;
   const SeqRange s = seq_range(a.start, a.count, b, a.N, c.cap);
-  const int blk = (s.start >> c.block_log2) + blockIdx.x;
+  const int blk = (s.start >> c.block_log2) + (int)(g >> 1);
   const int t0 = blk << c.block_log2;
   const int lo = max(s.start, t0), hi = min(s.start + s.n, t0 + (1 << c.block_log2));
   if (lo >= hi) return;
@@ -224,28 +225,40 @@ static __global__ void __launch_bounds__(512) kv_block_append_kernel(const KvApp
 // ------------------------------------------------------------------ read
 
 constexpr int kKrThreads = 256;
-constexpr int kKrPieces = 2;          // 16-code pieces of K and of V a thread has in flight
+constexpr int kKrPieces = 1;          // 16-code pieces of K and of V a thread takes (2, 4: no faster, longer for few tokens)
 
+// 16 values of a row; wide: in 32-byte stores, which write whole sectors (a
+// lane's neighbours are 32 or 64 bytes away).
 template <typename T>
-__device__ __forceinline__ void store16(T* dst, const float* f);
+__device__ __forceinline__ void store16(T* dst, const float* f, bool wide);
 template <>
-__device__ __forceinline__ void store16<__nv_bfloat16>(__nv_bfloat16* dst, const float* f) {
+__device__ __forceinline__ void store16<__nv_bfloat16>(__nv_bfloat16* dst, const float* f, bool wide) {
+  uint32_t r[8];
 #pragma unroll
-  for (int e = 0; e < 2; ++e)
-    __stcs(reinterpret_cast<uint4*>(dst) + e,
-           make_uint4(f2_to_bf2(f[8 * e], f[8 * e + 1]), f2_to_bf2(f[8 * e + 2], f[8 * e + 3]),
-                      f2_to_bf2(f[8 * e + 4], f[8 * e + 5]), f2_to_bf2(f[8 * e + 6], f[8 * e + 7])));
+  for (int e = 0; e < 8; ++e) r[e] = f2_to_bf2(f[2 * e], f[2 * e + 1]);
+  if (wide) {
+    store_32b(dst, r);
+  } else {
+    reinterpret_cast<uint4*>(dst)[0] = make_uint4(r[0], r[1], r[2], r[3]);
+    reinterpret_cast<uint4*>(dst)[1] = make_uint4(r[4], r[5], r[6], r[7]);
+  }
 }
 template <>
-__device__ __forceinline__ void store16<float>(float* dst, const float* f) {
+__device__ __forceinline__ void store16<float>(float* dst, const float* f, bool wide) {
+  const uint32_t* r = reinterpret_cast<const uint32_t*>(f);
+  if (wide) {
+    store_32b(dst, r);
+    store_32b(dst + 8, r + 8);
+  } else {
 #pragma unroll
-  for (int e = 0; e < 4; ++e)
-    __stcs(reinterpret_cast<float4*>(dst) + e, make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]));
+    for (int e = 0; e < 4; ++e)
+      reinterpret_cast<float4*>(dst)[e] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
+  }
 }
 
 // x = code * scale (one fp32 product, rounded once to T) of tokens [0, len) of
 // each sequence, zeros from len to the output's end.  A thread takes 16-code
-// pieces in output order (d, head, token), so a CTA's 512 pieces are a few
+// pieces in output order (d, head, token), so a CTA's 256 pieces are a few
 // consecutive tokens of all heads: contiguous stores, and loads of whole rows
 // of a block.  Bound by HBM.
 template <typename T, int KIND>
@@ -295,12 +308,12 @@ static __global__ void __launch_bounds__(kKrThreads) kv_block_read_kernel(const 
       for (int e = 0; e < 4; ++e) codes4_to_f<KIND>(k4[e], f + 4 * e);
 #pragma unroll
       for (int e = 0; e < 16; ++e) f[e] *= ks[i];
-      store16<T>(static_cast<T*>(a.k.ptr) + ko[i], f);
+      store16<T>(static_cast<T*>(a.k.ptr) + ko[i], f, a.wide);
 #pragma unroll
       for (int e = 0; e < 4; ++e) codes4_to_f<KIND>(v4[e], f + 4 * e);
 #pragma unroll
       for (int e = 0; e < 16; ++e) f[e] *= vs[i];
-      store16<T>(static_cast<T*>(a.v.ptr) + vo[i], f);
+      store16<T>(static_cast<T*>(a.v.ptr) + vo[i], f, a.wide);
     }
   }
 }

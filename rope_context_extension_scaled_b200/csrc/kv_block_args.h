@@ -29,6 +29,7 @@ struct KvReadArgs {
   KvBlockView c;
   const int64_t* len;               // [B]
   int n, d_log2, b0;
+  int wide;                         // output rows are 32-byte aligned
 };
 
 struct KvAttnArgs {

@@ -95,7 +95,7 @@ constexpr int kKvTcMinTiles = 3;
 constexpr int kKvTcStartTiles = 4;
 constexpr int kKvTcMergeTiles = 4;
 constexpr int kKvMaxSlice = 4096;      // sequences a launch takes
-constexpr int kKvReadPerCta = 512;     // 16-code pieces a CTA of the read kernel takes
+constexpr int kKvReadPerCta = 256;     // 16-code pieces a CTA of the read kernel takes
 int attn_kv_block_launch_int8(const KvAttnArgs& a, cudaStream_t stream);
 int attn_kv_block_launch_e4m3(const KvAttnArgs& a, cudaStream_t stream);
 int attn_kv_block_tc_launch(const KvAttnArgs& a, int kind, cudaStream_t stream);

@@ -14,9 +14,10 @@
 // (float64 product and reduction, see rope_cos_sin) and applies them to its
 // share of the heads, kRaGroup heads' loads in flight at a time.  With many
 // tokens a thread takes all heads, so that an angle is paid once per
-// Hq + Hkv vectors; with few tokens (decoding) the heads are dealt over
-// gridDim.y, because the call is then bound by the latency of a thread's loop
-// over the heads and the repeated angles are free.
+// Hq + Hkv vectors; with fewer the heads are dealt over gridDim.y until the GPU
+// has several waves of CTAs (16,384 tokens x 40 heads in fp32: 75 us as one wave
+// and a seventh, 4.5 TB/s), and with few (decoding) because the call is bound by
+// the latency of a thread's loop over the heads, where repeated angles are free.
 #pragma once
 #include "rope_apply.cuh"
 
@@ -31,13 +32,14 @@ struct RopeAxesArgs {
   int units;                        // units per head: d / 2 / pairs per unit
   int heads_per_y;                  // heads each blockIdx.y takes
   int halves, inverse;
+  int wide;                         // adjacent pairs in 32-byte aligned rows: both vectors at once
   Freqs f;
   uint8_t axis[kMaxPairs];
 };
 
 constexpr int kRaThreads = 128;
 constexpr int kRaGroup = 4;         // heads in flight: two 16-byte vectors each
-constexpr int kRaCtasPerSm = 8;     // grid: SMs x 8
+constexpr int kRaCtasPerSm = 32;    // CTAs an SM gets at least, where heads can be dealt out for it
 
 template <typename T>
 __device__ __forceinline__ void rope_unit(uint4& u, uint4& w, const float2* cs, bool halves);
@@ -103,8 +105,8 @@ __global__ void __launch_bounds__(kRaThreads) rope_axes_kernel(const RopeAxesArg
   const T* ki = static_cast<const T*>(a.k_in.ptr);
   T* qo = static_cast<T*>(a.q_out.ptr);
   T* ko = static_cast<T*>(a.k_out.ptr);
-  const int64_t step = (int64_t)gridDim.x * tpb;
-  for (int64_t n = (int64_t)blockIdx.x * tpb + threadIdx.x / units; n < a.n_tok; n += step) {
+  const int64_t n = (int64_t)blockIdx.x * tpb + threadIdx.x / units;
+  if (n < a.n_tok) {
     const int64_t b = a.N == a.n_tok ? 0 : n / a.N;
     const int64_t nn = n - b * a.N;
     const int64_t qin0 = b * a.q_in.sb + nn * a.q_in.sn, qout0 = b * a.q_out.sb + nn * a.q_out.sn;
@@ -118,8 +120,15 @@ __global__ void __launch_bounds__(kRaThreads) rope_axes_kernel(const RopeAxesArg
         const int h = h0 + g;
         if (h < h_hi) {
           const T* src = h < hq ? qi + qin0 + h * a.q_in.sh : ki + kin0 + (h - hq) * a.k_in.sh;
-          u[g] = __ldcs(reinterpret_cast<const uint4*>(src + e0));
-          w[g] = __ldcs(reinterpret_cast<const uint4*>(src + e1));
+          if (a.wide) {
+            uint32_t r[8];
+            load_32b(r, src + e0);
+            u[g] = make_uint4(r[0], r[1], r[2], r[3]);
+            w[g] = make_uint4(r[4], r[5], r[6], r[7]);
+          } else {
+            u[g] = __ldcs(reinterpret_cast<const uint4*>(src + e0));
+            w[g] = __ldcs(reinterpret_cast<const uint4*>(src + e1));
+          }
         }
       }
       if (h0 == h_lo) {                         // angles while the first loads are in flight
@@ -136,8 +145,13 @@ __global__ void __launch_bounds__(kRaThreads) rope_axes_kernel(const RopeAxesArg
         if (h < h_hi) {
           rope_unit<T>(u[g], w[g], cs, a.halves);
           T* dst = h < hq ? qo + qout0 + h * a.q_out.sh : ko + kout0 + (h - hq) * a.k_out.sh;
-          *reinterpret_cast<uint4*>(dst + e0) = u[g];
-          *reinterpret_cast<uint4*>(dst + e1) = w[g];
+          if (a.wide) {
+            const uint32_t r[8] = {u[g].x, u[g].y, u[g].z, u[g].w, w[g].x, w[g].y, w[g].z, w[g].w};
+            store_32b(dst + e0, r);
+          } else {
+            *reinterpret_cast<uint4*>(dst + e0) = u[g];
+            *reinterpret_cast<uint4*>(dst + e1) = w[g];
+          }
         }
       }
     }
