@@ -41,9 +41,7 @@ constexpr float kKbUp = 7.f;                    // P is held times 2^7
 template <int D>
 constexpr int kb_stage_bytes = 2 * kKbKeys * D;
 template <int D, int NT>
-constexpr int kb_stages = kv_few_stages(D, NT);
-template <int D, int NT>
-constexpr int kb_smem_bytes = kKbWarps * kb_stages<D, NT> * kb_stage_bytes<D> + NT * (D / 16) * 32 * 8 + NT * 8 * 4;
+constexpr int kb_smem_bytes = kKbWarps * kKvFewStages * kb_stage_bytes<D> + NT * (D / 16) * 32 * 8 + NT * 8 * 4;
 
 // 16-byte piece p of key row r sits at piece p ^ kb_swz(r): conflict-free for
 // the 8-row ldmatrix reads and for the quarter-warp reads of two rows.
@@ -67,7 +65,7 @@ __global__ void __launch_bounds__(kKbWarps * 32, kv_few_ctas(D, NT)) attn_kv_blo
   static_assert(1 << LOGT == kKbKeys, "tile");
   constexpr int kChunks = D / 16;               // 16-dim MMA steps
   constexpr int kStage = kb_stage_bytes<D>;
-  constexpr int kKbStages = kb_stages<D, NT>;
+  constexpr int kKbStages = kKvFewStages;
   constexpr int kTile = kKbKeys * D;
   constexpr int kPieces = D / 16;               // 16-byte pieces per key row
   constexpr int kRowsPerCopy = 32 / kPieces;    // key rows one warp-wide 16-byte copy covers

@@ -83,9 +83,11 @@ constexpr int kKvFewRows = 64;         // rows (tokens x heads of a group) up to
 constexpr int kKvFewItemRows = 32;     // rows of an item of it, at most
 constexpr int kKvFewTile = 32;         // its key tile
 constexpr int kKvFewWarps = 4;         // warps of its CTA, a tile each
-// resident CTAs and copy stages of the kernel for head dim D and nt columns of 8 rows
-constexpr int kv_few_ctas(int D, int nt) { return 2; }
-constexpr int kv_few_stages(int D, int nt) { return 3; }
+// Resident CTAs for head dim D and nt columns of 8 rows.  Registers allow four at
+// d = 64 with one column (a 4096-token window over 24 sequences 43 -> 41 us), two
+// elsewhere; three at d = 128 would need a two-stage ring (no faster).
+constexpr int kv_few_ctas(int D, int nt) { return D == 64 && nt == 1 ? 4 : 2; }
+constexpr int kKvFewStages = 3;        // of 32-key tiles in flight a warp
 constexpr int kKvFewMinTiles = 4;      // tiles a CTA takes at least
 constexpr int kKvFewStartTiles = 24;   // beginning an item costs a CTA as much as so many tiles
 constexpr int kKvFewMergeTiles = 6;    // what a scan and a merge cost, in tile times (see kv_attn_impl)
