@@ -345,8 +345,9 @@ typedef struct {
  * behind the new tokens, and blocks that get none, stay as they are.
  *
  * k, v: new tokens [B, N, Hkv, d], bf16 or f32 (one dtype), 16-byte aligned base
- * and strides; row i of sequence b is its token start[b] + i.  start, count:
- * device int64 [B]; count NULL means N each.  Reads each value and writes each
+ * and strides; row i of sequence b is its token start[b] + i; N at most the
+ * tokens a table row holds.  start, count: device int64 [B]; count NULL means N
+ * each.  Reads each value and writes each
  * code once.  Launches are timed under RCX_KERNEL_DECODE.
  */
 int rcx_kv_block_append(rcx_tensor k, rcx_tensor v, const rcx_kv_blocks* cache, const int64_t* start,
@@ -374,8 +375,10 @@ int rcx_kv_block_read(const rcx_kv_blocks* cache, const int64_t* len, rcx_tensor
  * Hq that is a multiple of Hkv; o: same shape, bf16 (8-byte aligned) or f32
  * (16-byte); lse: [B, Hq, N, 1] fp32 or ptr NULL.  start, count as for append.
  * The logits are fp32 sums of exact products of q and the codes; softmax
- * weights enter the product with V in fp16 with fp32 sums.  Up to 32 rows
- * (N * Hq / Hkv) run on mma.sync and read each code once; more run on tcgen05.
+ * weights enter the product with V in fp16 with fp32 sums.  Up to 64 rows
+ * (N * Hq / Hkv) run on mma.sync and read each code once; more run on tcgen05
+ * (the workspace of 2048 and more then holds an fp16 copy of the cached tokens
+ * that a table row has room for, where that is at most 1 GiB a sequence).
  * Results do not depend on what else runs: the split of the keys over the GPU
  * is fixed by the lengths, and partial results merge in a fixed order.
  * workspace: rcx_attn_kv_block_workspace_size(q, cache) bytes, 256-byte

@@ -471,9 +471,9 @@ def rope_axes_apply(q, k, inv_freq, axis, positions, halves=False, inverse=False
 
     Pair i turns by positions[axis[i], b, n] * inv_freq[i]; the pair is (i, i + d/2)
     with halves, else (2i, 2i + 1); inverse turns back, which is the gradient of
-    the rotation.  inv_freq [d/2] and axis [d/2] are host arrays, positions an
-    int64 [axes, B, N] tensor (axis and batch strides are free, 0 included).
-    Default: in place."""
+    the rotation (no autograd graph is recorded).  inv_freq [d/2] and axis [d/2]
+    are host arrays, positions an int64 [axes, B, N] tensor (axis and batch
+    strides are free, 0 included).  Default: in place."""
     if q is None and k is None:
         return None, None
     q_out = q if q_out is None else q_out
@@ -497,7 +497,15 @@ class KvBlockCache:
     float32 [n_blocks, Hkv].  table: int32 [B, width], the block of each
     sequence's tokens j * block ..; entries behind a sequence's tokens are not
     read.  The handle keeps the tensors, not their contents: tables and pools
-    are the caller's to fill and to change between calls."""
+    are the caller's to fill and to change between calls; other tensors need
+    another handle."""
+
+    __slots__ = ("k", "v", "k_scale", "v_scale", "table", "view", "address")
+
+    def __setattr__(self, name, value):
+        if hasattr(self, "address"):
+            raise AttributeError(f"a KvBlockCache does not change: make another one for another {name}")
+        object.__setattr__(self, name, value)
 
     def __init__(self, k, v, k_scale, v_scale, table):
         n, _, h, _ = k.shape

@@ -33,6 +33,11 @@
 //    8 of a bf16 output); when that grows, O shrinks by the same factor.
 //    A non-finite V scale counts as zero there and marks its 16 keys; a row
 //    that sees a marked key ends as NaN, and no other row does.
+// Converting a tile in every item that sees it is right for few row tiles; the
+// conversion then costs a third of the softmax's issue slots.  For many (2048
+// rows a sequence and more, kv_attn_impl) the tiles are converted once, before
+// the launch, into images of the swizzled shared-memory tiles (kv_block_expand),
+// and the producer copies those (KIND 2, no converters).
 // Every mbarrier wait is bounded, as in attn_tc.cuh.
 #pragma once
 #include <type_traits>
@@ -46,8 +51,11 @@ constexpr int kBtN = kKvTcTile;                 // keys per tile
 constexpr int kBtLogN = 7;
 static_assert(1 << kBtLogN == kBtN && 2 * kBtM == kKvTcRows, "tile");
 constexpr int kBtThreads = 512;
-constexpr int kBtRegsSoftmax = 200, kBtRegsConv = 72, kBtRegsMma = 40;
-static_assert(128 * (2 * kBtRegsSoftmax + kBtRegsConv + kBtRegsMma) <= 512 * 128, "registers of the launch");
+template <int KIND>
+struct BtRegs {                                 // registers a thread after the split
+  static constexpr int softmax = KIND == 2 ? 216 : 200, conv = KIND == 2 ? 40 : 72, mma = 40;
+  static_assert(128 * (2 * softmax + conv + mma) <= 512 * 128, "registers of the launch");
+};
 constexpr int kBtConv = 8;                      // first converter warp
 constexpr int kBtMma = 12;
 constexpr int kBtProd = 13;
@@ -58,6 +66,7 @@ constexpr uint32_t kBtHalf = kBtM * 128;        // 128 rows x 64 fp16, one swizz
 
 // The fp16 V tile holds value * this / (256 for e4m3) / (largest V scale): at
 // most 127 * 2^8 or 1.75 * 2^15, as far from fp16's subnormals as it goes.
+// KIND: 0 int8, 1 e4m3 codes, 2 tiles converted before the launch.
 template <int KIND>
 constexpr float kBtVUp = KIND == 0 ? 256.f : 32768.f;
 
@@ -151,6 +160,85 @@ __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.al
 template <int R>
 __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
 
+// Largest finite V scale of each sequence's visible blocks and KV head (the vref
+// of KIND 2).  One CTA each.
+static __global__ void __launch_bounds__(256) kv_block_vmax_kernel(const KvAttnArgs a) {
+  __shared__ uint32_t sm[8];
+  const int hk = blockIdx.x, b = a.b0 + blockIdx.y;
+  const SeqRange s = seq_range(a.start, a.count, b, a.N, a.c.cap);
+  const int blocks = s.n > 0 ? (s.start + s.n - 1 >> a.c.block_log2) + 1 : 0;
+  const int lo = a.window > 0 ? max(0, s.start + 1 - a.window) : 0;
+  const int first = lo >> a.c.block_log2, sinks = (min(a.n_sink, lo) + (1 << a.c.block_log2) - 1) >> a.c.block_log2;
+  uint32_t m = 0;
+#pragma unroll 4
+  for (int j = threadIdx.x; j < blocks; j += 256) {
+    if (j < first && j >= sinks) continue;
+    const int e = a.c.table[b * a.c.t_sb + j];
+    if ((unsigned)e >= (unsigned)a.c.n_blocks) continue;         // reported by the kernels that read it
+    const float v = a.c.vs[(int64_t)e * a.c.Hkv + hk];
+    if (v > 0.f && v < INFINITY) m = max(m, __float_as_uint(v));
+  }
+  m = __reduce_max_sync(0xffffffffu, m);
+  if (threadIdx.x % 32 == 0) sm[threadIdx.x / 32] = m;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int i = 1; i < 8; ++i) m = max(m, sm[i]);
+    a.img_vref[(int64_t)blockIdx.y * a.c.Hkv + hk] = __uint_as_float(m);
+  }
+}
+
+// Images of the swizzled fp16 K and V tiles of 128 keys, once per tile that a row
+// sees: [sequence, KV head, tile, K | V].  One CTA of 256 threads each; bound by
+// HBM (a byte in, two out).
+template <int D, int KIND>
+static __global__ void __launch_bounds__(256) kv_block_expand_kernel(const KvAttnArgs a) {
+  constexpr int kPieces = D / 16;
+  constexpr uint32_t kTile = BtSmem<D>::tile;
+  const KvBlockView& kv = a.c;
+  const int t = blockIdx.x, hk = blockIdx.y, bl = blockIdx.z, b = a.b0 + bl;
+  const SeqRange s = seq_range(a.start, a.count, b, a.N, kv.cap);
+  const int hi = s.start + s.n;
+  if (s.n == 0 || t * kBtN >= hi) return;
+  const int lo = a.window > 0 ? max(0, s.start + 1 - a.window) : 0;
+  if ((t + 1) * kBtN <= lo && t * kBtN >= min(a.n_sink, lo)) return;
+  const float vref = a.img_vref[(int64_t)bl * kv.Hkv + hk];
+  uint8_t* img = a.img + (((int64_t)bl * kv.Hkv + hk) * a.img_tiles + t) * 2 * kTile;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < kBtN * kPieces; i += 256) {
+    const int row = i / kPieces, pc = i % kPieces, key = t * kBtN + row;
+    uint4 x = make_uint4(0u, 0u, 0u, 0u), y = x;
+    float sv = 0.f;
+    if (key < hi) {
+      const int e = checked_block(kv, b, key >> kv.block_log2);
+      const int64_t r = key & ((1 << kv.block_log2) - 1);
+      if (e >= 0) {
+        x = __ldcs(reinterpret_cast<const uint4*>(kv.k + e * kv.k_sb + r * kv.k_sn + hk * kv.k_sh + pc * 16));
+        y = __ldcs(reinterpret_cast<const uint4*>(kv.v + e * kv.v_sb + r * kv.v_sn + hk * kv.v_sh + pc * 16));
+        sv = kv.vs[(int64_t)e * kv.Hkv + hk];
+      }
+    }
+    const float ratio = vref > 0.f && sv > 0.f && sv < INFINITY ? sv / vref * kBtVUp<KIND> : 0.f;
+    const __half2 rh = __float2half2_rn(ratio);
+    const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+    uint32_t h[8], g[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      codes4_to_h2<KIND>(xw[e], h[2 * e], h[2 * e + 1]);
+      codes4_to_h2<KIND>(yw[e], g[2 * e], g[2 * e + 1]);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const __half2 z = __hmul2(*reinterpret_cast<const __half2*>(&g[e]), rh);
+      g[e] = *reinterpret_cast<const uint32_t*>(&z);
+    }
+    const uint32_t at = (pc >> 2) * kBtHalf + row * 128, c0 = ((2 * (pc & 3)) ^ (row & 7)) * 16, c1 = c0 ^ 16;
+    *reinterpret_cast<uint4*>(img + at + c0) = make_uint4(h[0], h[1], h[2], h[3]);
+    *reinterpret_cast<uint4*>(img + at + c1) = make_uint4(h[4], h[5], h[6], h[7]);
+    *reinterpret_cast<uint4*>(img + kTile + at + c0) = make_uint4(g[0], g[1], g[2], g[3]);
+    *reinterpret_cast<uint4*>(img + kTile + at + c1) = make_uint4(g[4], g[5], g[6], g[7]);
+  }
+}
+
 template <int D, int KIND>
 __global__ void __launch_bounds__(kBtThreads, 1) attn_kv_block_tc_kernel(const __grid_constant__ KvAttnArgs a) {
   using L = BtSmem<D>;
@@ -190,7 +278,7 @@ __global__ void __launch_bounds__(kBtThreads, 1) attn_kv_block_tc_kernel(const _
       uint32_t cnt = 1;
       if (i < 2 || (i >= B_KFULL && i < B_KFULL + kBtStages) || (i >= B_VFULL && i < B_VFULL + kBtStages) ||
           i == B_PREADY || i == B_PREADY + 1 || i == B_REMPTY || i == B_REMPTY + 1)
-        cnt = 4;
+        cnt = KIND == 2 && i >= B_KFULL && i < B_PREADY ? 1 : 4;
       mbar_init(BAR(i), cnt);
     }
     *abort_flag = 0;
@@ -218,7 +306,7 @@ __global__ void __launch_bounds__(kBtThreads, 1) attn_kv_block_tc_kernel(const _
   bool ok = true;
 
   if (warp >= kBtMma) {
-    regs_down<kBtRegsMma>();
+    regs_down<BtRegs<KIND>::mma>();
     if (warp == kBtMma) {
     // ================================================================ MMA issuer
     constexpr uint32_t id_qk = idesc_f16(false, kBtN);
@@ -306,6 +394,7 @@ __global__ void __launch_bounds__(kBtThreads, 1) attn_kv_block_tc_kernel(const _
     const KvBlockView& kv = a.c;
     const int lb = kv.block_log2, bmask = (1 << lb) - 1;
     const uint32_t raw = sbase + L::raw;
+    (void)raw;
     int jg = 0, sent[2] = {0, 0};                 // tiles; K and V tiles whose copies were issued
     // lane i < 8: block of 16-key group i of tile u (0 behind the keys)
     auto load_phys = [&](int u, int u1) {
@@ -330,27 +419,43 @@ __global__ void __launch_bounds__(kBtThreads, 1) attn_kv_block_tc_kernel(const _
       return sc;
     };
     // codes of tile u's keys in the sequence -> raw rows; what stands in the other
-    // rows converts to finite numbers too, and their weights are zero
+    // rows converts to finite numbers too, and their weights are zero.  (KIND 2:
+    // the tile's image -> its stage.)
     auto copy_codes = [&](int u, int ph, int isv) {
-      const uint8_t* base = isv ? kv.v + w->hk * kv.v_sh : kv.k + w->hk * kv.k_sh;
-      const int64_t sb = isv ? kv.v_sb : kv.k_sb, sn = isv ? kv.v_sn : kv.k_sn;
-      const uint32_t dst = raw + isv * kBtN * D, bar = BAR(B_RFULL + isv);
-      const int key0 = w->span.tile(u) << kBtLogN;
-      const int rows = min(w->span.hi - key0, kBtN);
-      const int64_t off = ph * sb + ((key0 + 16 * (lane & 7)) & bmask) * sn;     // of the lane's group
-      if (lane == 0) mbar_expect_tx(bar, rows * D);
-      __syncwarp();
-      if (sn == D) {
-        const int n = min(rows - 16 * lane, 16);
-        if (lane < 8 && n > 0) bulk_load(dst + 16 * lane * D, base + off, n * D, bar);
+      if constexpr (KIND == 2) {
+        const int st = jg % kBtStages;
+        if (lane == 0) {
+          const uint32_t bar = BAR((isv ? B_VFULL : B_KFULL) + st);
+          const int64_t tile = ((int64_t)(w->b - a.b0) * kv.Hkv + w->hk) * a.img_tiles + w->span.tile(u);
+          mbar_expect_tx(bar, L::tile);
+          bulk_load(sbase + (isv ? L::v : L::k) + st * L::tile, a.img + (2 * tile + isv) * L::tile, L::tile, bar);
+        }
       } else {
-        for (int i = 0; i < kBtN / 32; ++i) {
-          const int r = 32 * i + lane;
-          const int64_t o = __shfl_sync(0xffffffffu, off, r >> 4) + (r & 15) * sn;
-          if (r < rows) bulk_load(dst + r * D, base + o, D, bar);
+        const uint8_t* base = isv ? kv.v + w->hk * kv.v_sh : kv.k + w->hk * kv.k_sh;
+        const int64_t sb = isv ? kv.v_sb : kv.k_sb, sn = isv ? kv.v_sn : kv.k_sn;
+        const uint32_t dst = raw + isv * kBtN * D, bar = BAR(B_RFULL + isv);
+        const int key0 = w->span.tile(u) << kBtLogN;
+        const int rows = min(w->span.hi - key0, kBtN);
+        const int64_t off = ph * sb + ((key0 + 16 * (lane & 7)) & bmask) * sn;     // of the lane's group
+        if (lane == 0) mbar_expect_tx(bar, rows * D);
+        __syncwarp();
+        if (sn == D) {
+          const int n = min(rows - 16 * lane, 16);
+          if (lane < 8 && n > 0) bulk_load(dst + 16 * lane * D, base + off, n * D, bar);
+        } else {
+          for (int i = 0; i < kBtN / 32; ++i) {
+            const int r = 32 * i + lane;
+            const int64_t o = __shfl_sync(0xffffffffu, off, r >> 4) + (r & 15) * sn;
+            if (r < rows) bulk_load(dst + r * D, base + o, D, bar);
+          }
         }
       }
       ++sent[isv];
+    };
+    // until K's (V's) place for tile jg is free
+    auto wait_place = [&](int isv) {
+      if constexpr (KIND == 2) return warp_wait((isv ? B_VEMPTY : B_KEMPTY) + jg % kBtStages, ((jg / kBtStages) & 1) ^ 1);
+      else return warp_wait(B_REMPTY + isv, (jg & 1) ^ 1);
     };
     while (ok && bt_next(w, a, lane)) {
       const int u0 = w->u0, u1 = u0 + w->n;
@@ -360,7 +465,7 @@ __global__ void __launch_bounds__(kBtThreads, 1) attn_kv_block_tc_kernel(const _
       for (int u = u0; u < u1; ++u, ++jg) {
         const int ph_next2 = load_phys(u + 2, u1);
         const float sc_next = load_scale(u + 1, u1, ph_next);
-        if (!(ok = warp_wait(B_REMPTY, (jg & 1) ^ 1))) break;
+        if (!(ok = wait_place(0))) break;
         copy_codes(u, ph, 0);
         // V scales: running maximum, ratios in fp16 (lanes 8-15 hold the groups')
         const bool is_v = lane >= 8 && lane < 16;
@@ -368,23 +473,24 @@ __global__ void __launch_bounds__(kBtThreads, 1) attn_kv_block_tc_kernel(const _
         const float sv = is_v && !bad ? sc : 0.f;
         const float vmax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(sv, 0.f))));
         const uint32_t vbad = (__ballot_sync(0xffffffffu, bad) >> 8) & 0xffu;
-        const float vnew = fmaxf(vref, vmax);
+        const float vnew = KIND == 2 ? a.img_vref[(int64_t)(w->b - a.b0) * kv.Hkv + w->hk] : fmaxf(vref, vmax);
         const float ratio = vnew > 0.f ? sv / vnew * kBtVUp<KIND> : 0.f;
         // the slot's last reader was the softmax of tile jg - 8: the copies above waited
         // for K of jg - 1 to be read, so K of jg - 2 stands in its stage and S of jg - 4
-        // is done, which came after both slots' weights of jg - 5
+        // is done, which came after both slots' weights of jg - 5 (KIND 2: for S of
+        // jg - 2, after their weights of jg - 3)
         BtMeta* mt = meta + jg % kBtMeta;
         if (lane < 8) mt->ks[lane] = sc;
         if (is_v) mt->ratio[lane - 8] = f2_to_h2(ratio, ratio);
         if (lane == 0) {
-          mt->vfac = vnew > 0.f ? vref / vnew : 1.f;
+          mt->vfac = KIND != 2 && vnew > 0.f ? vref / vnew : 1.f;
           mt->vbad = vbad;
           mt->vref = vnew;
         }
         vref = vnew;
         __syncwarp();
         if (lane == 0) mbar_arrive(BAR(B_META + jg % kBtMeta));
-        if (!(ok = warp_wait(B_REMPTY + 1, (jg & 1) ^ 1))) break;
+        if (!(ok = wait_place(1))) break;
         copy_codes(u, ph, 1);                     // its arrival also publishes the ratios
         ph = ph_next;
         ph_next = ph_next2;
@@ -392,13 +498,19 @@ __global__ void __launch_bounds__(kBtThreads, 1) attn_kv_block_tc_kernel(const _
       }
     }
     if (*abort_flag && lane == 0)                 // copies in flight land before the CTA ends
-      for (int i = 0; i < 2; ++i)
-        if (sent[i]) mbar_wait(BAR(B_RFULL + i), (sent[i] - 1) & 1, abort_flag, 100000000ull, false);
+      for (int i = 0; i < 2; ++i) {
+        if constexpr (KIND == 2) {
+          for (int n = max(0, sent[i] - kBtStages); n < sent[i]; ++n)
+            mbar_wait(BAR((i ? B_VFULL : B_KFULL) + n % kBtStages), (n / kBtStages) & 1, abort_flag, 100000000ull, false);
+        } else if (sent[i]) {
+          mbar_wait(BAR(B_RFULL + i), (sent[i] - 1) & 1, abort_flag, 100000000ull, false);
+        }
+      }
     __syncwarp();
     }
   } else if (warp >= kBtConv) {
     // ================================================================ converters
-    regs_down<kBtRegsConv>();
+    regs_down<BtRegs<KIND>::conv>();
     const int tid = threadIdx.x - kBtConv * 32;
     constexpr int kRows = 128 / kPieces;          // key rows the 128 threads cover at once
     // Piece pc of key rows i * kRows + pr.  Eight lanes take the pieces of one half
@@ -420,7 +532,7 @@ __global__ void __launch_bounds__(kBtThreads, 1) attn_kv_block_tc_kernel(const _
         const uint32_t wv[4] = {x.x, x.y, x.z, x.w};
         uint32_t h[8];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) codes4_to_h2<KIND>(wv[e], h[2 * e], h[2 * e + 1]);
+        for (int e = 0; e < 4; ++e) codes4_to_h2<KIND == 2 ? 0 : KIND>(wv[e], h[2 * e], h[2 * e + 1]);
         if constexpr (decltype(scaled)::value) {
           const uint32_t rb = ratios[(i * kRows + pr) >> 4];
           const __half2 rh = *reinterpret_cast<const __half2*>(&rb);
@@ -435,7 +547,7 @@ __global__ void __launch_bounds__(kBtThreads, 1) attn_kv_block_tc_kernel(const _
       }
     };
     int jg = 0;
-    while (ok && bt_next(w, a, lane)) {
+    while (KIND != 2 && ok && bt_next(w, a, lane)) {
       const int end = jg + w->n;
       for (; jg < end; ++jg) {
         const int st = jg % kBtStages;
@@ -452,7 +564,7 @@ __global__ void __launch_bounds__(kBtThreads, 1) attn_kv_block_tc_kernel(const _
     }
   } else {
     // ================================================================ softmax + epilogue
-    regs_up<kBtRegsSoftmax>();
+    regs_up<BtRegs<KIND>::softmax>();
     const int s = warp / 4;                     // slot of this warpgroup
     const int q4 = warp % 4;                    // TMEM lane quarter
     const int r = q4 * 32 + lane;               // row within the slot
@@ -495,7 +607,7 @@ __global__ void __launch_bounds__(kBtThreads, 1) attn_kv_block_tc_kernel(const _
       }
       float up, down;
       row_pow2(mx, up, down);
-      fac = down * a.scale_log2 * (KIND == 1 ? kE4m3Unscale : 1.f);
+      fac = down * a.scale_log2 * (KIND == 2 ? a.k_unscale : KIND == 1 ? kE4m3Unscale : 1.f);
       uint8_t* qrow = smem + L::q + s * L::tile + r * 128;
 #pragma unroll
       for (int i = 0; i < D / 8; ++i) {
@@ -647,7 +759,7 @@ __global__ void __launch_bounds__(kBtThreads, 1) attn_kv_block_tc_kernel(const _
       whole = w->whole;
       row_ok = s * kBtM + r < w->rows;
       const float lse = l == 0.f ? -INFINITY : (m_used - kKbUp + log2f(l)) * 0.69314718055994530942f;
-      inv = (l == 0.f ? 0.f : vref * ((KIND == 1 ? kE4m3Unscale : 1.f) / kBtVUp<KIND>) / l) + poison;
+      inv = (l == 0.f ? 0.f : vref * (KIND == 2 ? a.v_unscale : (KIND == 1 ? kE4m3Unscale : 1.f) / kBtVUp<KIND>) / l) + poison;
       prow = ((int64_t)blockIdx.x * 2 + w->slot) * a.rows_item + s * kBtM + r;
       off = (int64_t)w->b * a.o.sb + (int64_t)tok * a.o.sn + (int64_t)hq * a.o.sh;
       if (row_ok) {

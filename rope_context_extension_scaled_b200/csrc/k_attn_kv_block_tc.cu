@@ -14,7 +14,28 @@ static int kb_tc_launch(const KvAttnArgs& a, cudaStream_t stream) {
   return launch_status();
 }
 
-int attn_kv_block_tc_launch(const KvAttnArgs& a, int kind, cudaStream_t stream) {
+// K and V tiles of a.img (a.k_unscale, a.v_unscale: what they are to be multiplied by).
+template <int D, int KIND>
+static int kb_expand(KvAttnArgs& a, cudaStream_t stream) {
+  LaunchScope scope(RCX_KERNEL_DECODE, stream);
+  a.k_unscale = KIND == 1 ? kE4m3Unscale : 1.f;
+  a.v_unscale = a.k_unscale / kBtVUp<KIND>;
+  kv_block_vmax_kernel<<<dim3((unsigned)a.c.Hkv, (unsigned)a.B), 256, 0, stream>>>(a);
+  const int st = launch_status();
+  if (st) return st;
+  kv_block_expand_kernel<D, KIND><<<dim3((unsigned)a.img_tiles, (unsigned)a.c.Hkv, (unsigned)a.B), 256, 0, stream>>>(a);
+  return launch_status();
+}
+
+int attn_kv_block_tc_launch(const KvAttnArgs& args, int kind, cudaStream_t stream) {
+  KvAttnArgs a = args;
+  if (a.img) {
+    const int st = a.q.D == 64 ? (kind == 0 ? kb_expand<64, 0>(a, stream) : kb_expand<64, 1>(a, stream))
+                               : (kind == 0 ? kb_expand<128, 0>(a, stream) : kb_expand<128, 1>(a, stream));
+    if (st) return st;
+    LaunchScope scope(RCX_KERNEL_ATTN_TC, stream);
+    return a.q.D == 64 ? kb_tc_launch<64, 2>(a, stream) : kb_tc_launch<128, 2>(a, stream);
+  }
   LaunchScope scope(RCX_KERNEL_ATTN_TC, stream);
   if (a.q.D == 64) return kind == 0 ? kb_tc_launch<64, 0>(a, stream) : kb_tc_launch<64, 1>(a, stream);
   return kind == 0 ? kb_tc_launch<128, 0>(a, stream) : kb_tc_launch<128, 1>(a, stream);

@@ -52,6 +52,10 @@ struct KvAttnArgs {
   float* part_o;                    // [n_cta, 2, rows_item, d]: partials of items that several CTAs share
   float* part_lse;                  // [n_cta, 2, rows_item]
   int* prefix;                      // [B * n_rt + 2] first key tile of each (sequence, row tile); pieces of an item
+  uint8_t* img;                     // tiles converted before the launch, or null
+  float* img_vref;                  // [B, Hkv] V scale their V tiles are relative to
+  int img_tiles;                    // tiles a sequence and head has room for
+  float k_unscale, v_unscale;       // factors of the converted K and V values
   int64_t inject_spins;             // test hook of the tensor-core kernel
 };
 

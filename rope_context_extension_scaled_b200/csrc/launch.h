@@ -79,7 +79,10 @@ int quantize_i8_launch(const QuantArgs& a, bool rows16, int grid, cudaStream_t s
 // ---- k_kv_block.cu, k_attn_kv_block_*.cu (kind: 0 int8, 1 e4m3 codes)
 int kv_block_append_launch(const KvAppendArgs& a, int dtype, int kind, dim3 grid, int block, cudaStream_t stream);
 int kv_block_read_launch(const KvReadArgs& a, int dtype, int kind, dim3 grid, cudaStream_t stream);
-constexpr int kKvFewRows = 64;         // rows (tokens x heads of a group) up to which the mma.sync kernel runs
+// Rows (tokens x heads of a group) up to which the mma.sync kernel runs.  Its time
+// and the tcgen05 kernel's, d = 128, over 512 and 8192 tokens: 64 rows (8 sequences
+// of 4 heads) 19 and 60 us against 21 and 58, 96 rows 19 and 74 against 22 and 59.
+constexpr int kKvFewRows = 64;
 constexpr int kKvFewItemRows = 32;     // rows of an item of it, at most
 constexpr int kKvFewTile = 32;         // its key tile
 constexpr int kKvFewWarps = 4;         // warps of its CTA, a tile each
@@ -93,6 +96,12 @@ constexpr int kKvFewStartTiles = 24;   // beginning an item costs a CTA as much 
 constexpr int kKvFewMergeTiles = 6;    // what a scan and a merge cost, in tile times (see kv_attn_impl)
 constexpr int kKvTcRows = 256;         // rows of an item of the tcgen05 kernel, and its key tile
 constexpr int kKvTcTile = 128;
+// Rows of a sequence from which its tiles are converted once, before the launch,
+// where they fit kKvPreBytes (two bytes a code).  Without and with it, 8 heads,
+// d = 128: 2048 rows over 8192 tokens 143 and 126 us, 4000 rows 247 and 189 us,
+// 32,768 rows over 32,768 tokens 5.6 and 3.8 ms; 1024 rows 76 and 79 us.
+constexpr int kKvPreRows = 2048;
+constexpr int64_t kKvPreBytes = int64_t(1) << 30;
 constexpr int kKvTcMinTiles = 3;
 constexpr int kKvTcStartTiles = 4;
 constexpr int kKvTcMergeTiles = 4;

@@ -726,9 +726,9 @@ int kv_read_impl(const rcx_kv_blocks* cache, const int64_t* len, const rcx_tenso
 
 // Which kernel runs, how many sequences a launch takes, and the workspace.
 struct KvAttnPlan {
-  bool few;
-  int rows_item, n_rt, n_cta;
-  int64_t slice, off_lse, off_prefix, total;
+  bool few, pre;                    // pre: tiles are converted before the launch
+  int rows_item, n_rt, n_cta, img_tiles;
+  int64_t slice, off_lse, off_prefix, off_vref, off_img, total;
 };
 
 int kv_attn_plan(const rcx_tensor& q, const KvBlockView& c, int64_t B, KvAttnPlan* p) {
@@ -748,11 +748,17 @@ int kv_attn_plan(const rcx_tensor& q, const KvBlockView& c, int64_t B, KvAttnPla
   const int64_t tiles = (int64_t)c.Hkv * p->n_rt * (((int64_t)c.cap + tile - 1) / tile + 1);
   if (tiles > 0x7fffffff) return RCX_ERR_UNSUPPORTED;    // the kernels count tiles in 32 bits
   p->slice = std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(B, kKvMaxSlice), 0x7fffffff / tiles));
+  p->img_tiles = (int)(((int64_t)c.cap + kKvTcTile - 1) / kKvTcTile);
+  const int64_t img = (int64_t)p->img_tiles * c.Hkv * 2 * kKvTcTile * D * 2;      // of one sequence
+  p->pre = rows >= kKvPreRows && img <= kKvPreBytes;
+  if (p->pre) p->slice = std::min<int64_t>(p->slice, kKvPreBytes / img);
   const int64_t ctas = (int64_t)sm_count() * (p->few ? kv_few_ctas((int)D, p->rows_item / 8) : 1);
   p->n_cta = (int)std::min<int64_t>(ctas, p->slice * tiles);
   p->off_lse = align256((int64_t)p->n_cta * 2 * p->rows_item * D * 4);
   p->off_prefix = align256(p->off_lse + (int64_t)p->n_cta * 2 * p->rows_item * 4);
-  p->total = align256(p->off_prefix + (p->slice * p->n_rt + 2) * 4);
+  p->off_vref = align256(p->off_prefix + (p->slice * p->n_rt + 2) * 4);
+  p->off_img = align256(p->off_vref + (p->pre ? p->slice * c.Hkv * 4 : 0));
+  p->total = align256(p->off_img + (p->pre ? p->slice * img : 0));
   return RCX_OK;
 }
 
@@ -800,6 +806,11 @@ int kv_attn_impl(const rcx_tensor& q, const rcx_kv_blocks* cache, const int64_t*
   a.part_o = reinterpret_cast<float*>(ws);
   a.part_lse = reinterpret_cast<float*>(ws + p.off_lse);
   a.prefix = reinterpret_cast<int*>(ws + p.off_prefix);
+  if (p.pre) {
+    a.img = reinterpret_cast<uint8_t*>(ws + p.off_img);
+    a.img_vref = reinterpret_cast<float*>(ws + p.off_vref);
+    a.img_tiles = p.img_tiles;
+  }
   a.inject_spins = p.few ? 0 : attn_tc_inject();
   // Most key tiles an item can have: all its rows' windows and the sinks.
   const int64_t tile = p.few ? kKvFewTile : kKvTcTile;

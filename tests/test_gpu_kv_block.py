@@ -237,8 +237,9 @@ def test_single_tokens(kind, block, d, Hq, Hkv, start):
 
 @pytest.mark.parametrize("kind", ["int8", "e4m3"])
 @pytest.mark.parametrize("block,d,Hq,Hkv,N,start,count", [
-    (16, 128, 8, 2, 8, [0, 40, 3, 900], [8, 0, 5, 8]),          # 32 rows: the last of the one kernel
-    (16, 128, 11, 1, 3, [0, 40, 3, 900], [3, 0, 1, 3]),         # 33: the first of the other
+    (16, 128, 8, 2, 8, [0, 40, 3, 900], [8, 0, 5, 8]),          # 32 rows: one item of the one kernel
+    (16, 128, 11, 1, 3, [0, 40, 3, 900], [3, 0, 1, 3]),         # 33: two
+    (16, 128, 32, 2, 4, [0, 1000], [4, 3]), (64, 64, 5, 1, 13, [50, 0], [13, 12]),    # 64, and 65: the other kernel
     (32, 64, 8, 1, 16, [5, 0], [16, 9]), (32, 64, 43, 1, 3, [130, 2], [3, 2]),     # 128 and 129 rows
     (64, 128, 4, 1, 64, [64, 0, 1], [64, 33, 0]), (128, 64, 7, 1, 37, [1, 200], [37, 37]),   # 256 and 259
     (128, 128, 3, 3, 300, [0, 511], [300, 299]), (16, 64, 2, 1, 700, [0], [700]),
@@ -249,6 +250,33 @@ def test_drafts_and_chunks(kind, block, d, Hq, Hkv, N, start, count):
         pytest.fail("case")
     q, o, lse = attend(c, Hq, start, count, N, d)
     check_attention(c, q, o, lse, start, count)
+
+
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+@pytest.mark.parametrize("block,d,Hq,Hkv,N,start,count,window,n_sink", [
+    (16, 64, 48, 2, 86, [0, 300, 7], [86, 50, 0], 0, 0),        # 2064 rows: tiles converted before the launch
+    (64, 128, 16, 1, 140, [500, 0], [140, 139], 100, 40),
+    (128, 128, 16, 1, 128, [129, 1000], [128, 1], 0, 0),        # 2048, the first of them
+    (32, 64, 17, 1, 150, [2000], [150], 700, 0)])
+def test_many_rows_over_converted_tiles(kind, block, d, Hq, Hkv, N, start, count, window, n_sink):
+    c = filled([a + b for a, b in zip(start, count)], block, Hkv, d, kind, extra=1, spread=1.0)
+    row = c.table[len(start) - 1 if count[-1] else 0].long()
+    c.v_scale[row[:1]] = 0
+    for out in (None, torch.float32):
+        q, o, lse = attend(c, Hq, start, count, N, d, window=window, n_sink=n_sink, out=out)
+        check_attention(c, q, o, lse, start, count, window, n_sink)
+
+
+def test_nan_scale_over_converted_tiles():
+    start, N, G = 60, 140, 16
+    c = filled([start + N], 16, 1, 64, "e4m3")
+    q, o, lse = attend(c, G, [start], [N], N, 64)
+    c.v_scale[int(c.table[0, 96 // 16])] = float("nan")         # tokens 96 .. 111
+    _, o2, lse2 = attend(c, G, [start], [N], N, 64)
+    assert torch.isnan(o2[:, 36:]).all() and torch.equal(lse, lse2)
+    # the other rows: V tiles relative to another scale at most, two roundings of fp16 each
+    far = (o2[:, :36].double() - o[:, :36].double()).abs() - 2.0 ** -7 * o[:, :36].double().abs()
+    assert far.max() <= 6 * 2.0 ** -11 * np.abs(values(c, 0, 96)[1]).max()
 
 
 @pytest.mark.parametrize("N,Hq", [(1, 4), (4, 8), (50, 8)])
@@ -515,3 +543,5 @@ def test_python_refusals_on_the_gpu():
         _lib.kv_block_append(q, q, c, lens_of([3]))                        # four heads, two in the cache
     with pytest.raises(TypeError):
         _lib.attn_kv_block_fwd(q.half(), c, lens_of([3]))
+    with pytest.raises(AttributeError):
+        c.table = c.table.clone()                                          # the view would still name the old one
