@@ -449,7 +449,8 @@ __global__ void __launch_bounds__(kKbWarps * 32, kv_few_ctas(D, NT)) attn_kv_blo
 // and zeros (LSE -inf) for the rows of tokens past a sequence's count.  One CTA
 // per (entry, KV head) and slice of its rows; kWarpsPerRow warps share a row's
 // partials.  A warp reads 32 partials' LSE at once, then weighs their rows with
-// eight loads in flight: bound by the latency of that chain.  It waits for the
+// eight loads in flight (or all of up to four at once): bound by the latency of
+// that chain.  It waits for the
 // attention kernel's end on the device (programmatic dependent launch), so that
 // its launch is hidden behind it.
 template <int D, int kWarpsPerRow>
@@ -491,7 +492,26 @@ static __global__ void __launch_bounds__(256) attn_kv_block_merge_kernel(const K
     const bool shared = row_ok && r < live && c0 != c1;
     float mm = -INFINITY, lsum = 0.f;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (shared) {
+    if (shared && kWarpsPerRow == 1 && c1 - c0 < 4) {
+      // up to four partials, every lane on its own: all loads first
+      float ls[4];
+      float4 y[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int c = c0 + i;
+        const bool there = c <= c1 && (even == 0 || range_start(nt, i, even) < range_start(nt, i + 1, even));
+        const int64_t pr = ((int64_t)c * 2 + (i == 0 ? first_slot : 0)) * a.rows_item + r;
+        ls[i] = there ? a.part_lse[pr] : -INFINITY;
+        y[i] = there ? *reinterpret_cast<const float4*>(a.part_o + pr * D + dd) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      mm = fmaxf(fmaxf(ls[0], ls[1]), fmaxf(ls[2], ls[3]));                             // passes NaN over
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float wi = ls[i] == -INFINITY ? 0.f : expf(ls[i] - (mm == -INFINITY ? 0.f : mm));   // NaN stays here
+        lsum += wi;
+        x.x += wi * y[i].x; x.y += wi * y[i].y; x.z += wi * y[i].z; x.w += wi * y[i].w;
+      }
+    } else if (shared) {
       for (int cb = c0 + sub; cb <= c1; cb += 32 * kWarpsPerRow) {
         const int c = cb + kWarpsPerRow * lane;
         const int n = min(32, (c1 - cb) / kWarpsPerRow + 1);

@@ -127,10 +127,24 @@ template <> struct Piece16<__nv_bfloat16> {
     const uint32_t* w = reinterpret_cast<const uint32_t*>(u);
     return __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
   }
+  // fp32 bits of the largest magnitude, two elements an instruction
+  __device__ __forceinline__ uint32_t top() const {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(u);
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
+    return max(m & 0xffff0000u, m << 16);
+  }
 };
 template <> struct Piece16<float> {
   uint4 u[4];
   __device__ __forceinline__ float at(int i) const { return __uint_as_float(reinterpret_cast<const uint32_t*>(u)[i]); }
+  __device__ __forceinline__ uint32_t top() const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(at(i)) & 0x7fffffffu);
+    return m;
+  }
 };
 
 // One CTA per (block touched, KV head, K or V, sequence), block * d / 32 threads,
@@ -180,10 +194,7 @@ static __global__ void __launch_bounds__(512) kv_block_append_kernel(const KvApp
   }
 #pragma unroll
   for (int i = 0; i < 2; ++i)
-    if (fresh[i]) {
-#pragma unroll
-      for (int e = 0; e < 16; ++e) mx = max(mx, __float_as_uint(p[i].at(e)) & 0x7fffffffu);
-    }
+    if (fresh[i]) mx = max(mx, p[i].top());
   mx = __reduce_max_sync(0xffffffffu, mx);
   if ((tid & 31) == 0) sm_max[tid >> 5] = mx;
   __syncthreads();                                         // also: every thread has read the old scale
