@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(kKbWarps * 32, kv_few_ctas(D, NT)) attn_kv_blo
       float x[4 * kChunks];
       uint32_t mx = 0;
       if (r < t.rows) {
-        const int n = (t.r0 + r) / a.G, h = t.r0 + r - n * a.G;
+        const int n = (int)fast_div(t.r0 + r, a.div_g), h = t.r0 + r - n * a.G;
         const __nv_bfloat16* qp = static_cast<const __nv_bfloat16*>(a.q.ptr) + b * a.q.sb + (int64_t)n * a.q.sn +
                                   (int64_t)(w.hk * a.G + h) * a.q.sh + 16 * c;
 #pragma unroll
@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(kKbWarps * 32, kv_few_ctas(D, NT)) attn_kv_blo
       for (int h = 0; h < 2; ++h) {
         const int r = 8 * nt + 2 * c + h;
         fac[nt][h] = sm_fac[r];
-        qi[nt][h] = r < t.rows ? t.start + (t.r0 + r) / a.G : -1;
+        qi[nt][h] = r < t.rows ? t.start + (int)fast_div(t.r0 + r, a.div_g) : -1;
         m[nt][h] = -INFINITY;
         l[nt][h] = 0.f;
       }
@@ -399,16 +399,18 @@ __global__ void __launch_bounds__(kKbWarps * 32, kv_few_ctas(D, NT)) attn_kv_blo
         }
       }
     __syncthreads();
-    float* sm_o = reinterpret_cast<float*>(kb_smem);         // [warps][8 NT][D]
-    static_assert(kStage * kKbStages >= NT * 8 * D * 4, "merge area aliases the stage buffers");
+    // [warps][8 NT][D + 4]: the pad spreads the rows of a store over the banks
+    float* sm_o = reinterpret_cast<float*>(kb_smem);
+    constexpr int kRow = D + 4;
+    static_assert(kStage * kKbStages >= NT * 8 * kRow * 4, "merge area aliases the stage buffers");
     const float unscale = vref * (KIND == 1 ? kE4m3Unscale : 1.f);
 #pragma unroll
     for (int mt = 0; mt < kChunks; ++mt)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        float* w0 = sm_o + (warp * NT * 8 + 8 * nt + 2 * c) * D + 16 * mt + 2 * g;
+        float* w0 = sm_o + (warp * NT * 8 + 8 * nt + 2 * c) * kRow + 16 * mt + 2 * g;
         *reinterpret_cast<float2*>(w0) = make_float2(o[mt][nt][0] * unscale, o[mt][nt][2] * unscale);
-        *reinterpret_cast<float2*>(w0 + D) = make_float2(o[mt][nt][1] * unscale, o[mt][nt][3] * unscale);
+        *reinterpret_cast<float2*>(w0 + kRow) = make_float2(o[mt][nt][1] * unscale, o[mt][nt][3] * unscale);
       }
     __syncthreads();
     const bool whole = w.whole();
@@ -424,7 +426,7 @@ __global__ void __launch_bounds__(kKbWarps * 32, kv_few_ctas(D, NT)) attn_kv_blo
 #pragma unroll
       for (int x = 0; x < kKbWarps; ++x) {
         const float wt = dec_exp2(sm_m[x][r] - mr);
-        const float4 y = *reinterpret_cast<const float4*>(sm_o + (x * NT * 8 + r) * D + dd);
+        const float4 y = *reinterpret_cast<const float4*>(sm_o + (x * NT * 8 + r) * kRow + dd);
         lt += wt * sm_l[x][r];
         ot.x += wt * y.x; ot.y += wt * y.y; ot.z += wt * y.z; ot.w += wt * y.w;
       }
@@ -432,7 +434,7 @@ __global__ void __launch_bounds__(kKbWarps * 32, kv_few_ctas(D, NT)) attn_kv_blo
       ot.x *= inv; ot.y *= inv; ot.z *= inv; ot.w *= inv;
       const float lse = lt == 0.f ? -INFINITY : (mr - kKbUp + log2f(lt)) * 0.69314718055994530942f;
       if (whole) {
-        const int n = (t.r0 + r) / a.G, hq = w.hk * a.G + t.r0 + r - n * a.G;
+        const int n = (int)fast_div(t.r0 + r, a.div_g), hq = w.hk * a.G + t.r0 + r - n * a.G;
         store_o4(a, b * a.o.sb + (int64_t)n * a.o.sn + (int64_t)hq * a.o.sh + dd, ot);
         if (dd == 0 && a.lse) a.lse[b * a.lse_sb + hq * a.lse_sh + n] = lse;
       } else {
@@ -449,7 +451,7 @@ __global__ void __launch_bounds__(kKbWarps * 32, kv_few_ctas(D, NT)) attn_kv_blo
 // and zeros (LSE -inf) for the rows of tokens past a sequence's count.  One CTA
 // per (entry, KV head) and slice of its rows; kWarpsPerRow warps share a row's
 // partials.  A warp reads 32 partials' LSE at once, then weighs their rows with
-// eight loads in flight (or all of up to four at once): bound by the latency of
+// eight loads in flight (or all of up to eight at once): bound by the latency of
 // that chain.  It waits for the
 // attention kernel's end on the device (programmatic dependent launch), so that
 // its launch is hidden behind it.
@@ -462,8 +464,8 @@ static __global__ void __launch_bounds__(256) attn_kv_block_merge_kernel(const K
   const int e = blockIdx.x, hk = blockIdx.y;
   const int T = a.prefix[a.B * a.n_rt], p0 = a.prefix[e];
   const int nt = (a.prefix[e + 1] - p0) / a.c.Hkv;
-  const int rt = a.n_rt == 1 ? 0 : e % a.n_rt;
-  const int64_t b = a.b0 + (a.n_rt == 1 ? e : e / a.n_rt);
+  const int bl = (int)fast_div(e, a.div_nrt), rt = e - bl * a.n_rt;
+  const int64_t b = a.b0 + bl;
   const SeqRange s = seq_range(a.start, a.count, (int)b, a.N, a.c.cap);
   const int r0 = rt * a.rows_item;
   const int live = max(0, min(s.n * a.G - r0, a.rows_item));
@@ -492,21 +494,22 @@ static __global__ void __launch_bounds__(256) attn_kv_block_merge_kernel(const K
     const bool shared = row_ok && r < live && c0 != c1;
     float mm = -INFINITY, lsum = 0.f;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (shared && kWarpsPerRow == 1 && c1 - c0 < 4) {
-      // up to four partials, every lane on its own: all loads first
-      float ls[4];
-      float4 y[4];
+    if (shared && kWarpsPerRow == 1 && c1 - c0 < 8) {
+      // up to eight partials, every lane on its own: all loads first
+      float ls[8];
+      float4 y[8];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 8; ++i) {
         const int c = c0 + i;
         const bool there = c <= c1 && (even == 0 || range_start(nt, i, even) < range_start(nt, i + 1, even));
         const int64_t pr = ((int64_t)c * 2 + (i == 0 ? first_slot : 0)) * a.rows_item + r;
         ls[i] = there ? a.part_lse[pr] : -INFINITY;
         y[i] = there ? *reinterpret_cast<const float4*>(a.part_o + pr * D + dd) : make_float4(0.f, 0.f, 0.f, 0.f);
       }
-      mm = fmaxf(fmaxf(ls[0], ls[1]), fmaxf(ls[2], ls[3]));                             // passes NaN over
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 8; ++i) mm = fmaxf(mm, ls[i]);                                // passes NaN over
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
         const float wi = ls[i] == -INFINITY ? 0.f : expf(ls[i] - (mm == -INFINITY ? 0.f : mm));   // NaN stays here
         lsum += wi;
         x.x += wi * y[i].x; x.y += wi * y[i].y; x.z += wi * y[i].z; x.w += wi * y[i].w;
@@ -567,7 +570,7 @@ static __global__ void __launch_bounds__(256) attn_kv_block_merge_kernel(const K
       __syncthreads();
     }
     if (sub == 0 && row_ok && lane < kL && (shared || r >= live)) {
-      const int n = (r0 + r) / a.G, hq = hk * a.G + (r0 + r) - n * a.G;
+      const int n = (int)fast_div(r0 + r, a.div_g), hq = hk * a.G + (r0 + r) - n * a.G;
       const float inv = lsum == 0.f ? 0.f : 1.f / lsum;
       store_o4(a, b * a.o.sb + (int64_t)n * a.o.sn + (int64_t)hq * a.o.sh + dd,
                make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv));

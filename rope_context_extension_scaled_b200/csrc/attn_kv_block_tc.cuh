@@ -588,11 +588,12 @@ __global__ void __launch_bounds__(kBtThreads, 1) attn_kv_block_tc_kernel(const _
         have = bt_next(w, a, lane);
       }
       if (!have) return false;
-      const int rr = row_of(), tok = rr / a.G, hq = w->hk * a.G + rr - tok * a.G;
+      const int rr = row_of(), tok = (int)fast_div(rr, a.div_g), hq = w->hk * a.G + rr - tok * a.G;
       gi = w->start + tok;
       // tiles of keys full_lo < key0 <= full_hi, and sink tiles, need no mask for the slot's rows
-      full_hi = w->start + (w->r0 + s * kBtM) / a.G + 1 - kBtN;
-      full_lo = a.window == 0 ? -1 : w->start + (w->r0 + min((s + 1) * kBtM, w->rows) - 1) / a.G - a.window;
+      full_hi = w->start + (int)fast_div(w->r0 + s * kBtM, a.div_g) + 1 - kBtN;
+      full_lo =
+          a.window == 0 ? -1 : w->start + (int)fast_div(w->r0 + min((s + 1) * kBtM, w->rows) - 1, a.div_g) - a.window;
       const uint4* qp = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q.ptr) + (int64_t)w->b * a.q.sb +
                                                        (int64_t)tok * a.q.sn + (int64_t)hq * a.q.sh);
       uint4 x[D / 8];
@@ -755,7 +756,7 @@ __global__ void __launch_bounds__(kBtThreads, 1) attn_kv_block_tc_kernel(const _
       // ---- epilogue: O / l -> the output row, or a partial for the merge
       if (!(ok = __all_sync(0xffffffffu, mbar_wait(BAR(B_OFINAL + s), segs & 1, abort_flag)))) break;
       tc_fence_after();
-      const int rr = row_of(), tok = rr / a.G, hq = w->hk * a.G + rr - tok * a.G;
+      const int rr = row_of(), tok = (int)fast_div(rr, a.div_g), hq = w->hk * a.G + rr - tok * a.G;
       whole = w->whole;
       row_ok = s * kBtM + r < w->rows;
       const float lse = l == 0.f ? -INFINITY : (m_used - kKbUp + log2f(l)) * 0.69314718055994530942f;

@@ -24,6 +24,28 @@ inline View4 make_view(const rcx_tensor& t) {
   return v;
 }
 
+// Unsigned division by a run-time constant d, exact for n < 2^31 (Granlund
+// and Montgomery, "Division by invariant integers using multiplication",
+// 1994): with l = ceil(log2 d), p = 31 + l and m = ceil(2^p / d) (< 2^32),
+// floor(n / d) = (n * m) >> p, because m = (2^p + e) / d with 0 <= e < d adds
+// n e / (d 2^p) < 2^(31 - p) <= 1 / d to n / d.
+struct FastDiv {
+  uint32_t m, p;
+};
+
+inline FastDiv make_fastdiv(uint32_t d) {
+  uint32_t l = 0;
+  while ((uint64_t(1) << l) < d) ++l;
+  FastDiv f;
+  f.p = 31 + l;
+  f.m = (uint32_t)(((uint64_t(1) << f.p) + d - 1) / d);
+  return f;
+}
+
+__device__ __forceinline__ uint32_t fast_div(uint32_t n, FastDiv f) {
+  return (uint32_t)(((uint64_t)n * f.m) >> f.p);
+}
+
 // Up to 128 pairs of rotation frequencies, passed by value in kernel params.
 constexpr int kMaxPairs = 128;
 struct Freqs {

@@ -41,13 +41,14 @@ int attn_kv_block_tc_launch(const KvAttnArgs& args, int kind, cudaStream_t strea
   return kind == 0 ? kb_tc_launch<128, 0>(a, stream) : kb_tc_launch<128, 1>(a, stream);
 }
 
-// Where CTAs are many times the items, so are their partials: eight warps share a
-// row's.  Otherwise an item is cut a few times: a warp a row, with as many CTAs
-// an item as fill the GPU once.
+// Where items are small and CTAs many times as many, so are a row's partials: eight
+// warps share them.  Otherwise a warp takes a row, with as many CTAs an item as
+// fill the GPU once (256 rows in 5 to 18 pieces: 41 us an attention call with eight
+// warps a row, 35 so).
 int attn_kv_block_merge_launch(const KvAttnArgs& a, cudaStream_t stream) {
   LaunchScope scope(RCX_KERNEL_DECODE, stream);
   const int64_t items = (int64_t)a.B * a.n_rt * a.c.Hkv;
-  const bool many = items * 16 <= a.n_cta;
+  const bool many = a.rows_item <= kKvFewItemRows && items * 16 <= a.n_cta;
   const int rows = std::min(a.N * a.G, a.rows_item);
   const int z = many ? rows : (int)std::min<int64_t>((rows + 7) / 8, std::max<int64_t>(4, 8 * sm_count() / items));
   cudaLaunchConfig_t cfg = {};

@@ -39,6 +39,8 @@ struct KvAttnArgs {
   KvBlockView c;
   const int64_t *start, *count;
   int B, N, G, b0;                  // B sequences from sequence b0 on
+  // by G, Hkv, n_rt and N (direct): a walk makes a dozen divisions on its way to the first load
+  FastDiv div_g, div_hkv, div_nrt, div_n;
   int window, n_sink;               // window 0 = none
   float scale_log2;                 // log2(e) / (sqrt(d) * t)
   int o_bf16;

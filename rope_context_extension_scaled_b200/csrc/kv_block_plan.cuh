@@ -13,9 +13,9 @@
 //
 // Beginning an item costs a CTA about start_tiles tiles (its queries, its first
 // table entries and keys, its end), so two cases are dealt out otherwise:
-//   even:    fewer items than CTAs, and alike: each item is cut into `even` equal
-//            pieces, one a CTA, where the largest piece is within start_tiles of
-//            an even share;
+//   even:    fewer items than CTAs: each item is cut into `even` equal pieces, one
+//            a CTA, where these can be as small as min_tiles or, with items that
+//            are alike, are within start_tiles of an even share;
 //   direct:  items too short to be worth cutting (decided on the host, which
 //            knows how long they can be): the line holds whole items, and there
 //            is nothing to scan and nothing to merge.
@@ -62,8 +62,8 @@ struct Entry {
 template <int LOGT>
 __device__ __forceinline__ Entry entry_of(const KvAttnArgs& a, int e) {
   Entry t;
-  const int rt = a.n_rt == 1 ? 0 : e % a.n_rt;
-  t.b = a.b0 + (a.n_rt == 1 ? e : e / a.n_rt);
+  const int bl = (int)fast_div(e, a.div_nrt), rt = e - bl * a.n_rt;
+  t.b = a.b0 + bl;
   const SeqRange s = seq_range(a.start, a.count, t.b, a.N, a.c.cap);
   t.start = s.start;
   t.r0 = rt * a.rows_item;
@@ -74,8 +74,8 @@ __device__ __forceinline__ Entry entry_of(const KvAttnArgs& a, int e) {
     t.span.sink_tiles = t.span.first = t.span.n = t.span.hi = 0;
     return t;
   }
-  t.n_lo = t.r0 / a.G;
-  t.n_hi = (t.r0 + t.rows - 1) / a.G;
+  t.n_lo = (int)fast_div(t.r0, a.div_g);
+  t.n_hi = (int)fast_div(t.r0 + t.rows - 1, a.div_g);
   t.span = key_span<LOGT>(s.start, t.n_lo, t.n_hi, a.window, a.n_sink);
   return t;
 }
@@ -88,10 +88,12 @@ __device__ __forceinline__ int range_start(int T, int i, int P) { return (int)((
 __device__ __forceinline__ int range_owner(int T, int x, int P) { return (int)((((int64_t)x + 1) * P - 1) / T); }
 
 // Pieces of each item (0: the line is cut), from the T tiles of `items` items of
-// at most `most` tiles each.
+// at most `most` tiles each: as small as min_tiles allows where there are CTAs
+// for that.
 __device__ __forceinline__ int even_pieces(const KvAttnArgs& a, int T, int items, int most) {
-  const int s = min(a.n_cta / items, max(1, most / a.min_tiles));
-  return s >= 1 && (most + s - 1) / s <= T / a.n_cta + a.start_tiles ? s : 0;
+  const int ctas = a.n_cta / items, s = max(1, most / a.min_tiles);
+  if (ctas >= s) return s;
+  return ctas >= 1 && (most + ctas - 1) / ctas <= T / a.n_cta + a.start_tiles ? ctas : 0;
 }
 
 // Where a CTA begins: entry e, tile `off` of its Hkv * span.n tiles, and the
@@ -108,8 +110,9 @@ __device__ __forceinline__ PlanStart plan_start(const KvAttnArgs& a, int cta, in
   p.even = 0;
   if (a.direct) {
     p.e = p.off = 0;
-    p.x0 = range_start(E * Hkv, cta, a.n_cta);
-    p.x1 = range_start(E * Hkv, cta + 1, a.n_cta);
+    const bool one = E * Hkv == a.n_cta;        // an item each: no 64-bit divisions on the way
+    p.x0 = one ? cta : range_start(E * Hkv, cta, a.n_cta);
+    p.x1 = one ? cta + 1 : range_start(E * Hkv, cta + 1, a.n_cta);
     return p;
   }
   int carry = 0, incl = 0, mine = 0, most = 0;
@@ -136,7 +139,7 @@ __device__ __forceinline__ PlanStart plan_start(const KvAttnArgs& a, int cta, in
   if (s > 0) {
     const int item = cta / s;
     p.even = 1;
-    p.e = item / Hkv;
+    p.e = (int)fast_div(item, a.div_hkv);
     p.off = item - p.e * Hkv;
     p.x0 = cta - item * s;
     p.x1 = s;
@@ -191,7 +194,7 @@ struct SegWalk {
     if (a.direct) {
       while (x < x1) {
         const int i = x++;
-        e = i / a.c.Hkv;
+        e = (int)fast_div(i, a.div_hkv);
         hk = i - e * a.c.Hkv;
         t = entry_of<LOGT>(a, e);
         u0 = 0;
@@ -239,8 +242,9 @@ struct SegWalk {
 // launches; the merge writes them otherwise).  A warp per token.
 template <int D>
 __device__ __forceinline__ void empty_rows(const KvAttnArgs& a, int warp, int n_warps, int lane) {
-  for (int64_t i = (int64_t)blockIdx.x * n_warps + warp; i < (int64_t)a.B * a.N; i += (int64_t)gridDim.x * n_warps) {
-    const int64_t b = a.b0 + i / a.N, n = i % a.N;
+  for (unsigned i = blockIdx.x * n_warps + warp; i < (unsigned)(a.B * a.N); i += gridDim.x * n_warps) {
+    const int bl = (int)fast_div(i, a.div_n);
+    const int64_t b = a.b0 + bl, n = i - bl * a.N;
     if (n < seq_range(a.start, a.count, (int)b, a.N, a.c.cap).n) continue;
     const int H = (int)a.q.H;
     for (int x = lane; x < H * (D / 4); x += 32) {

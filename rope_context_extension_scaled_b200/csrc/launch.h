@@ -104,7 +104,7 @@ constexpr int kKvPreRows = 2048;
 constexpr int64_t kKvPreBytes = int64_t(1) << 30;
 constexpr int kKvTcMinTiles = 3;
 constexpr int kKvTcStartTiles = 4;
-constexpr int kKvTcMergeTiles = 4;
+constexpr int kKvTcMergeTiles = 6;
 constexpr int kKvMaxSlice = 4096;      // sequences a launch takes
 constexpr int kKvReadPerCta = 256;     // 16-code pieces a CTA of the read kernel takes
 int attn_kv_block_launch_int8(const KvAttnArgs& a, cudaStream_t stream);

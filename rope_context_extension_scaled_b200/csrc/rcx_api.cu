@@ -316,10 +316,13 @@ int rope_axes_impl(const rcx_tensor& q, const rcx_tensor& k, const rcx_tensor& q
   auto wide = [](const rcx_tensor& t) { return !t.ptr || aligned_rows(t, 32); };
   a.wide = !a.halves && wide(q) && wide(k) && (!has_q || wide(q_out)) && (!has_k || wide(k_out));
   // One CTA column takes all heads once the tokens alone give every SM its CTAs;
-  // below that the heads are dealt out, kRaGroup at least to each.
+  // below that the heads are dealt out, kRaGroup at least to each, or two groups
+  // where the tokens alone give every SM a CTA (17,506 tokens x 12 bf16 heads: 21 us in one
+  // column, 28 in three, whose angles cost more than their loads).
   const int64_t want = (int64_t)sm_count() * kRaCtasPerSm;
   const int64_t groups = (heads + kRaGroup - 1) / kRaGroup;
-  const int64_t cols = std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(groups, 65535), want / passes));
+  const int64_t most = passes >= (int64_t)sm_count() ? std::max<int64_t>(1, groups / 2) : groups;
+  const int64_t cols = std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(most, 65535), want / passes));
   a.heads_per_y = (int)((groups + cols - 1) / cols) * kRaGroup;
   const int64_t nx = passes, ny = (heads + a.heads_per_y - 1) / a.heads_per_y;
   return rope_axes_launch(a, dtype, dim3((unsigned)nx, (unsigned)ny), tpb * a.units, stream);
@@ -799,6 +802,10 @@ int kv_attn_impl(const rcx_tensor& q, const rcx_kv_blocks* cache, const int64_t*
   a.window = (int)std::min<int64_t>(window, 0x7fffffff);
   a.n_sink = (int)std::min<int64_t>(n_sink, a.c.cap);
   a.scale_log2 = (float)(1.4426950408889634074 / (std::sqrt((double)D) * temperature));
+  a.div_g = make_fastdiv((uint32_t)a.G);
+  a.div_hkv = make_fastdiv((uint32_t)a.c.Hkv);
+  a.div_nrt = make_fastdiv((uint32_t)p.n_rt);
+  a.div_n = make_fastdiv((uint32_t)N);
   a.rows_item = p.rows_item;
   a.n_rt = p.n_rt;
   a.n_cta = p.n_cta;
@@ -830,7 +837,8 @@ int kv_attn_impl(const rcx_tensor& q, const rcx_kv_blocks* cache, const int64_t*
     const int64_t items = (int64_t)a.B * p.n_rt * a.c.Hkv;
     const int64_t per_item = (most + lanes - 1) / lanes;
     a.direct = (items + ctas - 1) / ctas * per_item <=
-               items * most / (ctas * lanes) + (p.few ? kKvFewMergeTiles : kKvTcMergeTiles);
+                   items * most / (ctas * lanes) + (p.few ? kKvFewMergeTiles : kKvTcMergeTiles) &&
+               a.B * N < 0x40000000;
     a.n_cta = a.direct ? (int)std::min<int64_t>(ctas, items) : p.n_cta;
     st = !p.few ? attn_kv_block_tc_launch(a, kind, stream)
          : kind == 0 ? attn_kv_block_launch_int8(a, stream) : attn_kv_block_launch_e4m3(a, stream);

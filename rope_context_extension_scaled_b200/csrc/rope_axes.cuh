@@ -39,7 +39,7 @@ struct RopeAxesArgs {
 
 constexpr int kRaThreads = 128;
 constexpr int kRaGroup = 4;         // heads in flight: two 16-byte vectors each
-constexpr int kRaCtasPerSm = 32;    // CTAs an SM gets at least, where heads can be dealt out for it
+constexpr int kRaCtasPerSm = 16;    // CTAs an SM gets at least, where heads can be dealt out for it
 
 template <typename T>
 __device__ __forceinline__ void rope_unit(uint4& u, uint4& w, const float2* cs, bool halves);
