@@ -684,13 +684,17 @@ __global__ void __launch_bounds__(kBtThreads, 1) attn_kv_block_tc_kernel(const _
           for (int c = 16 * q; c < 16 * q + 16; c += 2) mul2(x[c], x[c + 1], f);
         }
         if (!full) {
-          auto clip = [](int y) { return y < -1 ? -1 : (y > kBtN ? kBtN : y); };
-          const int lim = clip(gi - key0);
-          const int win_lo = a.window > 0 ? clip(gi - a.window - key0) : -1;
-          const int snk = a.window > 0 ? clip(a.n_sink - 1 - key0) : -1;
+          const int lim = gi - key0;            // columns up to here are the row's past
+          if (a.window == 0) {
 #pragma unroll
-          for (int c = 0; c < kBtN; ++c)
-            if (!(c <= lim && (c > win_lo || c <= snk))) x[c] = -INFINITY;
+            for (int c = 0; c < kBtN; ++c)
+              if (c > lim) x[c] = -INFINITY;
+          } else {
+            const int win_lo = gi - a.window - key0, snk = a.n_sink - 1 - key0;
+#pragma unroll
+            for (int c = 0; c < kBtN; ++c)
+              if (c > lim || (c <= win_lo && c > snk)) x[c] = -INFINITY;
+          }
         }
         if (mt->vbad) {                         // NaN for the rows that see a marked key
           for (int c = 0; c < kBtN; ++c)

@@ -799,7 +799,7 @@ int kv_attn_impl(const rcx_tensor& q, const rcx_kv_blocks* cache, const int64_t*
   a.count = count;
   a.N = (int)N;
   a.G = (int)(Hq / a.c.Hkv);
-  a.window = (int)std::min<int64_t>(window, 0x7fffffff);
+  a.window = window < a.c.cap ? (int)window : 0;          // a window of the whole table hides nothing
   a.n_sink = (int)std::min<int64_t>(n_sink, a.c.cap);
   a.scale_log2 = (float)(1.4426950408889634074 / (std::sqrt((double)D) * temperature));
   a.div_g = make_fastdiv((uint32_t)a.G);
@@ -823,7 +823,7 @@ int kv_attn_impl(const rcx_tensor& q, const rcx_kv_blocks* cache, const int64_t*
   const int64_t tile = p.few ? kKvFewTile : kKvTcTile;
   const int64_t rows_tok = std::min<int64_t>(N, p.rows_item / a.G + 2);
   int64_t reach = a.c.cap;
-  if (window > 0 && window < reach) reach = std::min<int64_t>(reach, window + rows_tok + a.n_sink + 2 * tile);
+  if (a.window > 0) reach = std::min<int64_t>(reach, window + rows_tok + a.n_sink + 2 * tile);
   const int64_t most = (reach + tile - 1) / tile;
   const int64_t lanes = p.few ? kKvFewWarps : 1;            // tiles a CTA works on at once
   const int64_t ctas = (int64_t)sm_count() * (p.few ? kv_few_ctas((int)D, p.rows_item / 8) : 1);
