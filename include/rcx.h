@@ -310,8 +310,8 @@ int rcx_attn_decode_int8_fwd(rcx_tensor q, rcx_tensor k, const float* k_scale, r
  * for both); block 16, 32, 64 or 128; d 64 or 128; stride[3] == 1, base pointers
  * and the other strides multiples of 16 bytes (the layout may be
  * [n_blocks, Hkv, block, d] underneath).  k_scale, v_scale: device fp32
- * [n_blocks, Hkv], contiguous.  table: device int32 [B, width]; entries of
- * blocks that hold no token of the sequence are not read.
+ * [n_blocks, Hkv], contiguous, never negative.  table: device int32 [B, width];
+ * entries of blocks that hold no token of the sequence are not read.
  *
  * Scale and code of a block whose largest |x| is amax (0: scale 0, codes 0):
  *   RCX_I8:   s = fl(amax / 127), at least 2^-120; code = rint(x * fl(1 / s)),

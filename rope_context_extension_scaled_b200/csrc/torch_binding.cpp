@@ -243,11 +243,13 @@ PyObject* attn_kv_block_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const long long window = integer(a[7]), n_sink = integer(a[8]);
     const double t = PyFloat_AsDouble(a[9]);
     if (t == -1.0 && PyErr_Occurred()) throw PyError();
+    const int want_lse = PyObject_IsTrue(a[11]);
+    if (want_lse < 0) throw PyError();
     OnDevice on(dev.index);
     const at::Tensor o = o_in ? *o_in : at::empty(q->sizes(), q->options());
     at::Tensor lse, ws;
     if (lse_in) lse = *lse_in;
-    else if (a[11] == Py_True) lse = at::empty({q->size(0), q->size(2), q->size(1)}, q->options().dtype(at::kFloat));
+    else if (want_lse) lse = at::empty({q->size(0), q->size(2), q->size(1)}, q->options().dtype(at::kFloat));
     if (ws_in) {
       ws = *ws_in;
       if (!ws.is_contiguous()) value_error("workspace must be contiguous");

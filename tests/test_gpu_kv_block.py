@@ -401,6 +401,32 @@ def test_many_sequences_and_long_split():
     check_attention(c, q, o, lse, start, count)
 
 
+def test_more_sequences_than_a_launch_takes():
+    """70,000 sequences of one token each, some with none: the attention of a single key is its value."""
+    B, d = 70000, 64
+    t = torch.randperm(B, generator=gen(1), device=DEV).int()[:, None].contiguous()
+    k = torch.zeros(B, 16, 1, d, dtype=torch.int8, device=DEV)
+    s = torch.full((B, 1), 9.0, device=DEV)
+    c = _lib.KvBlockCache(k, k.clone(), s, s.clone(), t)
+    x, y = (torch.randn(B, 1, 1, d, generator=gen(n), device=DEV) for n in (2, 3))
+    start, count = torch.zeros(B, dtype=torch.int64, device=DEV), torch.ones(B, dtype=torch.int64, device=DEV)
+    count[::7] = 0
+    _lib.kv_block_append(x, y, c, start, count)
+    kk, vv = _lib.kv_block_read(c, count, 1, dtype=torch.float32)
+    live = count.bool()
+    for got, want in ((kk, x), (vv, y)):                      # half a step of amax / 127
+        assert ((got - want).abs() <= want.abs().amax(-1, keepdim=True) * (0.5001 / 127))[live].all()
+        assert not got[~live].any()
+    assert (c.k_scale[t[~live].long().flatten()] == 9).all()
+    o, lse = _lib.attn_kv_block_fwd(x.to(torch.bfloat16), c, start, count, o=torch.empty_like(x))
+    # weight 2^7 p over its own sum and V as it stands: roundings of fp32 only
+    assert ((o - vv).abs() <= 2.0 ** -21 * vv.abs().amax(-1, keepdim=True))[live].all() and not o[~live].any()
+    z = (x.to(torch.bfloat16).double() * kk.double()).sum(-1).flatten() / 8
+    assert torch.isneginf(lse[~live]).all()
+    assert (lse.flatten().double() - z)[live].abs().max() <= (d + 8) * 2.0 ** -23 * 40 + 2.0 ** -20
+    assert _lib.device_status() == 0
+
+
 def test_positions_past_32_bit_offsets():
     """A pool of more than 2^31 bytes of codes: the last blocks are reached."""
     block, d, H = 128, 128, 8
