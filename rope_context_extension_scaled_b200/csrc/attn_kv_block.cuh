@@ -450,26 +450,26 @@ __global__ void __launch_bounds__(kKbWarps * 32, kv_few_ctas(D, NT)) attn_kv_blo
 // Merge of items that several CTAs share, by the LSE rule of rcx_merge_partials,
 // and zeros (LSE -inf) for the rows of tokens past a sequence's count.  One CTA
 // per (entry, KV head) and slice of its rows; kWarpsPerRow warps share a row's
-// partials.  A warp reads 32 partials' LSE at once, then weighs their rows with
-// eight loads in flight (or all of up to eight at once): bound by the latency of
-// that chain.  It waits for the
-// attention kernel's end on the device (programmatic dependent launch), so that
-// its launch is hidden behind it.
+// partials.  A warp loads up to eight partials at once; of more, 32 LSE at once and
+// then their rows with eight loads in flight: bound by the latency of that chain.
+// It waits for the attention kernel's end on the device (programmatic dependent
+// launch), so that its launch is hidden behind it.
 template <int D, int kWarpsPerRow>
 static __global__ void __launch_bounds__(256) attn_kv_block_merge_kernel(const KvAttnArgs a) {
   constexpr int kL = D / 4;                      // lanes that hold dims (d = 64: half a warp)
   __shared__ float sm_m[8], sm_l[8];
   __shared__ float4 sm_o[8][32];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int e = blockIdx.x, hk = blockIdx.y;
-  const int T = a.prefix[a.B * a.n_rt], p0 = a.prefix[e];
-  const int nt = (a.prefix[e + 1] - p0) / a.c.Hkv;
   const int bl = (int)fast_div(e, a.div_nrt), rt = e - bl * a.n_rt;
   const int64_t b = a.b0 + bl;
   const SeqRange s = seq_range(a.start, a.count, (int)b, a.N, a.c.cap);
   const int r0 = rt * a.rows_item;
   const int live = max(0, min(s.n * a.G - r0, a.rows_item));
   const int rows = min(a.N * a.G - r0, a.rows_item);
+  // lengths were there before the attention kernel began; its tables and partials come now
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int T = a.prefix[a.B * a.n_rt], p0 = a.prefix[e];
+  const int nt = (int)fast_div(a.prefix[e + 1] - p0, a.div_hkv);
   // CTAs c0 .. c1 hold pieces of the item; the first one's may be its range's last
   // segment (the line), all others are their CTA's first
   const int even = a.prefix[a.B * a.n_rt + 1];
@@ -494,15 +494,15 @@ static __global__ void __launch_bounds__(256) attn_kv_block_merge_kernel(const K
     const bool shared = row_ok && r < live && c0 != c1;
     float mm = -INFINITY, lsum = 0.f;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (shared && kWarpsPerRow == 1 && c1 - c0 < 8) {
-      // up to eight partials, every lane on its own: all loads first
+    if (shared && c1 - c0 < 8 * kWarpsPerRow) {
+      // up to eight partials a warp, every lane on its own: all loads first
       float ls[8];
       float4 y[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const int c = c0 + i;
-        const bool there = c <= c1 && (even == 0 || range_start(nt, i, even) < range_start(nt, i + 1, even));
-        const int64_t pr = ((int64_t)c * 2 + (i == 0 ? first_slot : 0)) * a.rows_item + r;
+        const int j = sub + kWarpsPerRow * i, c = c0 + j;
+        const bool there = c <= c1 && (even == 0 || nt >= even || range_start(nt, j, even) < range_start(nt, j + 1, even));
+        const int64_t pr = ((int64_t)c * 2 + (j == 0 ? first_slot : 0)) * a.rows_item + r;
         ls[i] = there ? a.part_lse[pr] : -INFINITY;
         y[i] = there ? *reinterpret_cast<const float4*>(a.part_o + pr * D + dd) : make_float4(0.f, 0.f, 0.f, 0.f);
       }
@@ -520,7 +520,7 @@ static __global__ void __launch_bounds__(256) attn_kv_block_merge_kernel(const K
         const int n = min(32, (c1 - cb) / kWarpsPerRow + 1);
         const int64_t pr = ((int64_t)c * 2 + (c == c0 ? first_slot : 0)) * a.rows_item + r;
         // (even: an item with fewer tiles than pieces leaves some without any)
-        const bool there = lane < n && (even == 0 || range_start(nt, c - c0, even) < range_start(nt, c - c0 + 1, even));
+        const bool there = lane < n && (even == 0 || nt >= even || range_start(nt, c - c0, even) < range_start(nt, c - c0 + 1, even));
         const float ls = there ? a.part_lse[pr] : -INFINITY;
         float mn = ls;
 #pragma unroll
