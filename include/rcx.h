@@ -327,7 +327,8 @@ int rcx_attn_decode_int8_fwd(rcx_tensor q, rcx_tensor k, const float* k_scale, r
  * [0, n_blocks) is not followed (append writes nothing there, read gives zeros,
  * attention uses block 0 instead), and rcx_device_status() reports
  * RCX_ERR_DEVICE_INDEX.  Calls that only read may share blocks between
- * sequences; a block that append writes must belong to one sequence.
+ * sequences; a block that append writes must belong to one sequence and stand
+ * once in its row.
  */
 typedef struct {
     rcx_tensor k, v;

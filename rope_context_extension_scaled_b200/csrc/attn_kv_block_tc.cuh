@@ -18,7 +18,7 @@
 //               shared memory (bulk copies of 16 tokens, or of a token where
 //               those are not contiguous) and works out its scales, so the
 //               cache is read as it is stored and never copied whole
-//   (14, 15 have nothing to do)
+//   (14, 15 zero the rows of tokens past a sequence's count, in direct launches)
 // The softmax threads hold a row of S: registers move to them from the other
 // warpgroups (setmaxnreg; 2 x 200, 72 and 40 a thread are the launch's 65,536),
 // and each warp's place in the walk over segments is kept in shared memory.
@@ -293,7 +293,6 @@ __global__ void __launch_bounds__(kBtThreads, 1) attn_kv_block_tc_kernel(const _
     }
   }
   if (warp == kBtMma) tmem_alloc(smem_addr(tmem_slot), 512);
-  if (a.direct) empty_rows<D>(a, warp, kBtThreads / 32, lane);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -507,6 +506,8 @@ __global__ void __launch_bounds__(kBtThreads, 1) attn_kv_block_tc_kernel(const _
         }
       }
     __syncwarp();
+    } else if (a.direct) {
+      empty_rows<D>(a, warp - kBtProd - 1, 2, lane);
     }
   } else if (warp >= kBtConv) {
     // ================================================================ converters
