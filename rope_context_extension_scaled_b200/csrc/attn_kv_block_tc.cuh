@@ -160,6 +160,16 @@ __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.al
 template <int R>
 __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
 
+// Blocks that the window hides from every row of a sequence: [sinks, first).
+struct HiddenBlocks {
+  int sinks, first;
+  __device__ __forceinline__ bool has(int j) const { return j >= sinks && j < first; }
+};
+__device__ __forceinline__ HiddenBlocks hidden_blocks(const KvAttnArgs& a, int start) {
+  const int lb = a.c.block_log2, lo = a.window > 0 ? max(0, start + 1 - a.window) : 0;
+  return {(min(a.n_sink, lo) + (1 << lb) - 1) >> lb, lo >> lb};
+}
+
 // Largest finite V scale of each sequence's visible blocks and KV head (the vref
 // of KIND 2).  One CTA each.
 static __global__ void __launch_bounds__(256) kv_block_vmax_kernel(const KvAttnArgs a) {
@@ -167,12 +177,11 @@ static __global__ void __launch_bounds__(256) kv_block_vmax_kernel(const KvAttnA
   const int hk = blockIdx.x, b = a.b0 + blockIdx.y;
   const SeqRange s = seq_range(a.start, a.count, b, a.N, a.c.cap);
   const int blocks = s.n > 0 ? (s.start + s.n - 1 >> a.c.block_log2) + 1 : 0;
-  const int lo = a.window > 0 ? max(0, s.start + 1 - a.window) : 0;
-  const int first = lo >> a.c.block_log2, sinks = (min(a.n_sink, lo) + (1 << a.c.block_log2) - 1) >> a.c.block_log2;
+  const HiddenBlocks hidden = hidden_blocks(a, s.start);
   uint32_t m = 0;
 #pragma unroll 4
   for (int j = threadIdx.x; j < blocks; j += 256) {
-    if (j < first && j >= sinks) continue;
+    if (hidden.has(j)) continue;
     const int e = a.c.table[b * a.c.t_sb + j];
     if ((unsigned)e >= (unsigned)a.c.n_blocks) continue;         // reported by the kernels that read it
     const float v = a.c.vs[(int64_t)e * a.c.Hkv + hk];
@@ -189,7 +198,8 @@ static __global__ void __launch_bounds__(256) kv_block_vmax_kernel(const KvAttnA
 
 // Images of the swizzled fp16 K and V tiles of 128 keys, once per tile that a row
 // sees: [sequence, KV head, tile, K | V].  One CTA of 256 threads each; bound by
-// HBM (a byte in, two out).
+// HBM (a byte in, two out).  Blocks of the tile that no row sees are zeros: vref
+// does not cover their scales, and a V beyond fp16 would make NaN of its weight 0.
 template <int D, int KIND>
 static __global__ void __launch_bounds__(256) kv_block_expand_kernel(const KvAttnArgs a) {
   constexpr int kPieces = D / 16;
@@ -202,13 +212,14 @@ static __global__ void __launch_bounds__(256) kv_block_expand_kernel(const KvAtt
   const int lo = a.window > 0 ? max(0, s.start + 1 - a.window) : 0;
   if ((t + 1) * kBtN <= lo && t * kBtN >= min(a.n_sink, lo)) return;
   const float vref = a.img_vref[(int64_t)bl * kv.Hkv + hk];
+  const HiddenBlocks hidden = hidden_blocks(a, s.start);
   uint8_t* img = a.img + (((int64_t)bl * kv.Hkv + hk) * a.img_tiles + t) * 2 * kTile;
 #pragma unroll 4
   for (int i = threadIdx.x; i < kBtN * kPieces; i += 256) {
     const int row = i / kPieces, pc = i % kPieces, key = t * kBtN + row;
     uint4 x = make_uint4(0u, 0u, 0u, 0u), y = x;
     float sv = 0.f;
-    if (key < hi) {
+    if (key < hi && !hidden.has(key >> kv.block_log2)) {
       const int e = checked_block(kv, b, key >> kv.block_log2);
       const int64_t r = key & ((1 << kv.block_log2) - 1);
       if (e >= 0) {

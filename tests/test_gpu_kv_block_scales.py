@@ -1,0 +1,82 @@
+"""Attention over the block-scaled cache where scales lie far apart: O is bounded
+by the values that a row sees, whatever stands in blocks that it does not see."""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import rcx_oracle as orc
+from rope_context_extension_scaled_b200 import _lib
+from tests._parity import np64
+from tests.test_gpu_kv_block import DEV, attend, filled, gen, lens_of, values
+
+pytestmark = pytest.mark.gpu
+
+
+def check_seen(c, q, o, lse, start, count, window=0, n_sink=0):
+    """O and LSE against the oracle, bounded by what each row sees.
+
+    A = the largest sum |q_i k_i| / sqrt(d) over the row's keys: logits are fp32
+    sums of d exact products and a few roundings of factors, delta = (d + 8)
+    2^-23 A.  A weight carries 2 delta, 2^-21 of the exponential and up to three
+    half steps of fp16 (weight, V tile, V ratio), times the largest |v| of the
+    row's keys; fp16's floor is 2^-25 of weights held as 2^7 p for a reference
+    scale at most 2^4 above the block's own: 2^-28 a key.  O is rounded once."""
+    N, Hq, d = q.shape[1:]
+    o_type = 2.0 ** -8 if o.dtype == torch.bfloat16 else 2.0 ** -22
+    for b in range(q.shape[0]):
+        n0, n = start[b], count[b]
+        og, lg = np64(o[b]), lse[b].double().cpu().numpy()
+        assert np.isfinite(og).all() and not og[n:].any() and np.isneginf(lg[:, n:]).all()
+        if n == 0:
+            continue
+        K, V = values(c, b, n0 + n)
+        qq = np64(q[b, :n])
+        i, j = n0 + np.arange(n)[:, None], np.arange(n0 + n)[None]
+        seen = (j <= i) & ((window == 0) | (j > i - window) | (j < n_sink))
+        O, L = orc.attention(qq, K, V, 1.0 / math.sqrt(d), window=window, n_sink=n_sink, q_index=n0 + np.arange(n),
+                             k_index=np.arange(n0 + n))
+        G = Hq // K.shape[1]
+        for h in range(Hq):
+            a = (np.abs(qq[:, h]) @ np.abs(K[:, h // G]).T) / math.sqrt(d)
+            delta = (d + 8) * 2.0 ** -23 * np.where(seen, a, 0).max(1)
+            top = np.where(seen, np.abs(V[:, h // G]).max(1)[None], 0).max(1)
+            tol = top * (2 * delta + 2.0 ** -21 + 3 * 2.0 ** -11 + (n0 + n) * 2.0 ** -28)
+            bad = np.abs(og[:n, h] - O[:, h]) - (o_type * np.abs(O[:, h]) + tol[:, None])
+            assert bad.max() <= 0, (b, h, np.unravel_index(bad.argmax(), bad.shape), bad.max())
+            far = np.abs(lg[h, :n] - L[h]) - (delta + 2.0 ** -21 + 2.0 ** -22 * np.abs(L[h]))
+            assert far.max() <= 0, (b, h, far.max())
+
+
+def unseen_blocks(n0, n, block, window, n_sink):
+    """Blocks of a sequence's tokens that none of its rows sees."""
+    first = max(0, n0 + 1 - window)
+    return [j for j in range(-(-(n0 + n) // block)) if (j + 1) * block <= first and j * block >= n_sink]
+
+
+def unseen_blocks(n0, n, block, window, n_sink):
+    """Blocks of a sequence's tokens that none of its rows sees."""
+    first = max(0, n0 + 1 - window)
+    return [j for j in range(-(-(n0 + n) // block)) if (j + 1) * block <= first and j * block >= n_sink]
+
+
+UNSEEN = [(16, 600, 100, 4), (32, 1000, 90, 40), (64, 600, 100, 4)]      # block, start, window, n_sink
+
+
+def unseen(kind, G, N, block, start, window, n_sink, factor):
+    """Windows and sinks that end inside a key tile: the scales of the tile's other blocks do not matter."""
+    c = filled([start + N], block, 1, 64, kind)
+    hidden = unseen_blocks(start, N, block, window, n_sink)
+    assert hidden
+    c.v_scale[c.table[0, hidden].long()] *= factor
+    q, o, lse = attend(c, G, [start], [N], N, 64, window=window, n_sink=n_sink)
+    check_seen(c, q, o, lse, [start], [N], window, n_sink)
+
+
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+@pytest.mark.parametrize("block,start,window,n_sink", UNSEEN)
+@pytest.mark.parametrize("power", [1, 2, 10, 70])
+def test_unseen_scales_over_converted_tiles(kind, block, start, window, n_sink, power):
+    unseen(kind, 16, 140, block, start, window, n_sink, 2.0 ** power)
