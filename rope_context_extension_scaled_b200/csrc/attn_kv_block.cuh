@@ -403,15 +403,22 @@ __global__ void __launch_bounds__(kKbWarps * 32, kv_few_ctas(D, NT)) attn_kv_blo
     float* sm_o = reinterpret_cast<float*>(kb_smem);
     constexpr int kRow = D + 4;
     static_assert(kStage * kKbStages >= NT * 8 * kRow * 4, "merge area aliases the stage buffers");
-    const float unscale = vref * (KIND == 1 ? kE4m3Unscale : 1.f);
+    // each warp's own average: it cannot pass the largest value, whereas sums of values of 2^112 and more can pass fp32
 #pragma unroll
-    for (int mt = 0; mt < kChunks; ++mt)
+    for (int nt = 0; nt < NT; ++nt) {
+      float av[2];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
+      for (int h = 0; h < 2; ++h) av[h] = l[nt][h] == 0.f ? 0.f : vref * (1.f / l[nt][h]);
+#pragma unroll
+      for (int mt = 0; mt < kChunks; ++mt) {
+        float y[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] = o[mt][nt][e] * av[e & 1] * (KIND == 1 ? kE4m3Unscale : 1.f);
         float* w0 = sm_o + (warp * NT * 8 + 8 * nt + 2 * c) * kRow + 16 * mt + 2 * g;
-        *reinterpret_cast<float2*>(w0) = make_float2(o[mt][nt][0] * unscale, o[mt][nt][2] * unscale);
-        *reinterpret_cast<float2*>(w0 + kRow) = make_float2(o[mt][nt][1] * unscale, o[mt][nt][3] * unscale);
+        *reinterpret_cast<float2*>(w0) = make_float2(y[0], y[2]);
+        *reinterpret_cast<float2*>(w0 + kRow) = make_float2(y[1], y[3]);
       }
+    }
     __syncthreads();
     const bool whole = w.whole();
     const int64_t prow = ((int64_t)blockIdx.x * 2 + w.slot()) * a.rows_item;
@@ -421,17 +428,17 @@ __global__ void __launch_bounds__(kKbWarps * 32, kv_few_ctas(D, NT)) attn_kv_blo
 #pragma unroll
       for (int x = 0; x < kKbWarps; ++x) mm = fmaxf(mm, sm_m[x][r]);
       const float mr = mm == -INFINITY ? 0.f : mm;
-      float lt = 0.f;
+      float lt = 0.f, wl[kKbWarps];
       float4 ot = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
+      for (int x = 0; x < kKbWarps; ++x) lt += wl[x] = dec_exp2(sm_m[x][r] - mr) * sm_l[x][r];
+      const float inv = lt == 0.f ? 0.f : 1.f / lt;
+#pragma unroll
       for (int x = 0; x < kKbWarps; ++x) {
-        const float wt = dec_exp2(sm_m[x][r] - mr);
+        const float wt = wl[x] * inv;
         const float4 y = *reinterpret_cast<const float4*>(sm_o + (x * NT * 8 + r) * kRow + dd);
-        lt += wt * sm_l[x][r];
         ot.x += wt * y.x; ot.y += wt * y.y; ot.z += wt * y.z; ot.w += wt * y.w;
       }
-      const float inv = lt == 0.f ? 0.f : 1.f / lt;
-      ot.x *= inv; ot.y *= inv; ot.z *= inv; ot.w *= inv;
       const float lse = lt == 0.f ? -INFINITY : (mr - kKbUp + log2f(lt)) * 0.69314718055994530942f;
       if (whole) {
         const int n = (int)fast_div(t.r0 + r, a.div_g), hq = w.hk * a.G + t.r0 + r - n * a.G;
@@ -452,6 +459,7 @@ __global__ void __launch_bounds__(kKbWarps * 32, kv_few_ctas(D, NT)) attn_kv_blo
 // per (entry, KV head) and slice of its rows; kWarpsPerRow warps share a row's
 // partials.  A warp loads up to eight partials at once; of more, 32 LSE at once and
 // then their rows with eight loads in flight: bound by the latency of that chain.
+// x is the average so far, not the sum: averages stay within the values' range.
 // It waits for the attention kernel's end on the device (programmatic dependent
 // launch), so that its launch is hidden behind it.
 template <int D, int kWarpsPerRow>
@@ -510,8 +518,13 @@ static __global__ void __launch_bounds__(256) attn_kv_block_merge_kernel(const K
       for (int i = 0; i < 8; ++i) mm = fmaxf(mm, ls[i]);                                // passes NaN over
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float wi = ls[i] == -INFINITY ? 0.f : expf(ls[i] - (mm == -INFINITY ? 0.f : mm));   // NaN stays here
-        lsum += wi;
+        ls[i] = ls[i] == -INFINITY ? 0.f : expf(ls[i] - (mm == -INFINITY ? 0.f : mm));            // NaN stays here
+        lsum += ls[i];
+      }
+      const float inv = lsum == 0.f ? 0.f : 1.f / lsum;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float wi = ls[i] * inv;
         x.x += wi * y[i].x; x.y += wi * y[i].y; x.z += wi * y[i].z; x.w += wi * y[i].w;
       }
     } else if (shared) {
@@ -526,13 +539,16 @@ static __global__ void __launch_bounds__(256) attn_kv_block_merge_kernel(const K
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));   // passes NaN over
         mn = fmaxf(mn, mm);
-        const float wt = ls == -INFINITY ? 0.f : expf(ls - (mn == -INFINITY ? 0.f : mn));        // NaN stays here
+        float wt = ls == -INFINITY ? 0.f : expf(ls - (mn == -INFINITY ? 0.f : mn));              // NaN stays here
         const float f0 = mm == mn ? 1.f : expf(mm - mn);
         float ws = wt;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) ws += __shfl_xor_sync(0xffffffffu, ws, o);
-        lsum = lsum * f0 + ws;
-        x.x *= f0; x.y *= f0; x.z *= f0; x.w *= f0;
+        const float kept = lsum * f0;
+        lsum = kept + ws;
+        const float inv = lsum == 0.f ? 0.f : 1.f / lsum, f1 = kept * inv;
+        wt *= inv;
+        x.x *= f1; x.y *= f1; x.z *= f1; x.w *= f1;
         mm = mn;
 #pragma unroll 8
         for (int i = 0; i < n; ++i) {
@@ -557,13 +573,18 @@ static __global__ void __launch_bounds__(256) attn_kv_block_merge_kernel(const K
         for (int i = 0; i < kWarpsPerRow; ++i) mt = fmaxf(mt, sm_m[warp + i]);
         x = make_float4(0.f, 0.f, 0.f, 0.f);
         lsum = 0.f;
+        float f[kWarpsPerRow];
 #pragma unroll
         for (int i = 0; i < kWarpsPerRow; ++i) {
-          if (sm_l[warp + i] == 0.f) continue;
-          const float f = expf(sm_m[warp + i] - (mt == -INFINITY ? 0.f : mt));
+          f[i] = sm_l[warp + i] == 0.f ? 0.f : expf(sm_m[warp + i] - (mt == -INFINITY ? 0.f : mt)) * sm_l[warp + i];
+          lsum += f[i];
+        }
+        const float inv = lsum == 0.f ? 0.f : 1.f / lsum;
+#pragma unroll
+        for (int i = 0; i < kWarpsPerRow; ++i) {
           const float4 y = sm_o[warp + i][lane];
-          x.x += f * y.x; x.y += f * y.y; x.z += f * y.z; x.w += f * y.w;
-          lsum += f * sm_l[warp + i];
+          const float wi = f[i] * inv;
+          x.x += wi * y.x; x.y += wi * y.y; x.z += wi * y.z; x.w += wi * y.w;
         }
         mm = mt;
       }
@@ -571,9 +592,7 @@ static __global__ void __launch_bounds__(256) attn_kv_block_merge_kernel(const K
     }
     if (sub == 0 && row_ok && lane < kL && (shared || r >= live)) {
       const int n = (int)fast_div(r0 + r, a.div_g), hq = hk * a.G + (r0 + r) - n * a.G;
-      const float inv = lsum == 0.f ? 0.f : 1.f / lsum;
-      store_o4(a, b * a.o.sb + (int64_t)n * a.o.sn + (int64_t)hq * a.o.sh + dd,
-               make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv));
+      store_o4(a, b * a.o.sb + (int64_t)n * a.o.sn + (int64_t)hq * a.o.sh + dd, x);
       if (lane == 0 && a.lse) a.lse[b * a.lse_sb + hq * a.lse_sh + n] = lsum == 0.f ? -INFINITY : mm + logf(lsum);
     }
   }

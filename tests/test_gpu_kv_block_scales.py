@@ -14,6 +14,10 @@ from tests.test_gpu_kv_block import DEV, attend, filled, gen, lens_of, values
 
 pytestmark = pytest.mark.gpu
 
+# (heads of the group, tokens): the mma.sync kernel with one and several columns, the
+# tcgen05 kernel with converters, and over tiles converted before the launch
+SHAPES = [(4, 1), (8, 8), (16, 10), (16, 140)]
+
 
 def check_seen(c, q, o, lse, start, count, window=0, n_sink=0):
     """O and LSE against the oracle, bounded by what each row sees.
@@ -80,3 +84,19 @@ def unseen(kind, G, N, block, start, window, n_sink, factor):
 @pytest.mark.parametrize("power", [1, 2, 10, 70])
 def test_unseen_scales_over_converted_tiles(kind, block, start, window, n_sink, power):
     unseen(kind, 16, 140, block, start, window, n_sink, 2.0 ** power)
+
+
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+@pytest.mark.parametrize("G,N", SHAPES)
+@pytest.mark.parametrize("start", [5, 3000, 40000])
+@pytest.mark.parametrize("alike", [False, True])
+def test_largest_scales_stay_finite(kind, G, N, start, alike):
+    """Values up to 2^127 (the format's largest scales), random or all the same: their averages are finite."""
+    c = filled([start + N], 64, 1, 64, kind)
+    c.v_scale.fill_(2.0 ** 120 if kind == "int8" else 2.0 ** 118)
+    if kind == "e4m3":
+        c.v.copy_(c.v.float().clamp(-240, 240).to(c.v.dtype))
+    if alike:
+        c.v.copy_(torch.full(c.v.shape, 120.0, device=DEV).to(c.v.dtype))
+    q, o, lse = attend(c, G, [start], [N], N, 64, out=torch.float32)
+    check_seen(c, q, o, lse, [start], [N])
