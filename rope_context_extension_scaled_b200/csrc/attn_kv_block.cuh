@@ -19,10 +19,13 @@
 //    pieces c and c + 4 of key rows g and g + 8, and Q is laid out to match.
 //  * V^T comes from ldmatrix.trans over 16-bit elements (two dims of one key).
 //  * The block scale of K multiplies S per 16 keys (blocks are 16 tokens or
-//    more); that of V multiplies P as ratio to the largest V scale met so far.
-//    P is held as 2^7 p in fp16 (p <= 2^8 between moves of m), so weights down
-//    to 2^-31 of the largest keep their place; 11 bits of P against 8 of a
-//    bf16 output.
+//    more); that of V multiplies P as ratio to vref, which follows the scales up
+//    and, past 2^-4 of it, down again (not below 2^-80 of the largest), O changing
+//    with it in fp32.  So P's range is spent on weights, whatever scales other rows
+//    see.  P is held as 2^7 p in fp16 (p <= 2^8 between moves of m): weights down
+//    to 2^-28 of the largest keep their place; 11 bits of P against 8 of a bf16
+//    output.
+//  * 16 keys that no row of the item sees are not read, nor is their table entry.
 //  * m moves only when a logit passes it by 2^8: most tiles need no shuffle
 //    and no rescale of O.
 // Table entries and scales come 16 tiles at a time, one per lane, a batch ahead.
@@ -58,6 +61,34 @@ __device__ __forceinline__ void row_pow2(uint32_t bits, float& up, float& down) 
   up = __uint_as_float((uint32_t)f << 23);
   down = __uint_as_float((uint32_t)(254 - f) << 23);
 }
+
+// Reference of the V scales: the first scale that is not zero times a power of two,
+// so that moving it is exact, and scales that are all alike are exact too.  Keys
+// of scales lo .. hi (positive) move it to hi or just above where hi passes it or
+// lo falls below 2^-4 of it, but not below 2^-80 of the largest so far.
+struct VRef {
+  float v, inv, top;
+  __device__ __forceinline__ bool holds(float lo, float hi) const { return hi <= v && lo * 16.f >= v; }
+  __device__ __forceinline__ void begin(float s) {
+    if (v > 0.f) return;
+    v = top = fmaxf(s, 0x1p-126f);
+    inv = 1.f / v;
+  }
+  // what O is to be multiplied by
+  __device__ __forceinline__ float move(float hi) {
+    const int want = __float_as_int(fminf(fmaxf(fmaxf(hi, top * 0x1p-80f), 0x1p-126f), 0x1p125f));
+    const int k = (want - __float_as_int(v) + 0x7fffff) >> 23;     // least k with v 2^k >= want
+    v = __int_as_float(__float_as_int(v) + (k << 23));
+    inv = __int_as_float(__float_as_int(inv) - (k << 23));
+    top = fmaxf(top, v);
+    return k > 126 ? 0.f : __int_as_float((127 - k) << 23);
+  }
+  __device__ __forceinline__ float follow(float s) {
+    if (!(s > 0.f)) return 1.f;                  // zero or NaN
+    begin(s);
+    return holds(s, s) ? 1.f : move(s);
+  }
+};
 
 template <int D, int NT, int KIND>
 __global__ void __launch_bounds__(kKbWarps * 32, kv_few_ctas(D, NT)) attn_kv_block_kernel(const KvAttnArgs a) {
@@ -108,13 +139,15 @@ __global__ void __launch_bounds__(kKbWarps * 32, kv_few_ctas(D, NT)) attn_kv_blo
     const int32_t* trow = kv.table + b * kv.t_sb;
     const float* ksh = kv.ks + w.hk;
     const float* vsh = kv.vs + w.hk;
+    // keys up to here, sinks apart, are outside every row's window
+    const int hidden = a.window > 0 ? t.start + t.n_lo - a.window : -1;
     auto load_meta = [&](int batch, int& ph, float& ks, float& vs) {
       ph = 0;
       ks = vs = 0.f;
       const int kk = 16 * batch + (lane >> 1);
       if (kk < nk) {
         const int key = (span.tile(ub + kKbWarps * kk) << LOGT) + ((lane & 1) << 4);
-        if (key < hi) {
+        if (key < hi && (key + 15 > hidden || key < a.n_sink)) {
           int e = trow[key >> lb];
           if ((unsigned)e >= (unsigned)kv.n_blocks) {
             record_device_error(RCX_ERR_DEVICE_INDEX);
@@ -224,7 +257,16 @@ __global__ void __launch_bounds__(kKbWarps * 32, kv_few_ctas(D, NT)) attn_kv_blo
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[mt][nt][e] = 0.f;
-    float vref = 0.f;                            // largest V scale met so far
+    VRef vref = {0.f, 0.f, 0.f};
+    bool uneven = false;                         // the reference moves tile by tile
+    auto scale_o = [&](float f) {
+#pragma unroll
+      for (int mt = 0; mt < kChunks; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[mt][nt][e] *= f;
+    };
 
     int st = 0;
     for (int kk = 0; kk < nk; ++kk) {
@@ -234,6 +276,16 @@ __global__ void __launch_bounds__(kKbWarps * 32, kv_few_ctas(D, NT)) attn_kv_blo
         ks_a = ks_b;
         vs_a = vs_b;
         load_meta(batch + 1, ph_b, ks_b, vs_b);
+      }
+      if ((kk & 15) == 0) {                      // the reference for 16 tiles at once, if one can hold them all
+        const uint32_t bits = vs_a > 0.f ? __float_as_uint(vs_a) : 0u;
+        const float hi = __uint_as_float(__reduce_max_sync(0xffffffffu, bits));
+        const float lo = __uint_as_float(__reduce_min_sync(0xffffffffu, bits ? bits : 0x7f7fffffu));
+        uneven = hi > 0.f && lo * 16.f < hi;
+        if (hi > 0.f && !uneven) {
+          vref.begin(__shfl_sync(0xffffffffu, vs_a, __ffs(__ballot_sync(0xffffffffu, bits != 0u)) - 1));
+          if (!vref.holds(lo, hi)) scale_o(vref.move(hi));
+        }
       }
       issue(kk + kKbStages - 1, batch, st == 0 ? kKbStages - 1 : st - 1);
       asm volatile("cp.async.wait_group %0;" ::"n"(kKbStages - 1) : "memory");
@@ -313,10 +365,15 @@ __global__ void __launch_bounds__(kKbWarps * 32, kv_few_ctas(D, NT)) attn_kv_blo
 #pragma unroll
         for (int h = 0; h < 2; ++h)
           move |= fmaxf(fmaxf(s[0][nt][h], s[0][nt][h + 2]), fmaxf(s[1][nt][h], s[1][nt][h + 2])) > m[nt][h] + kKbLazy;
-      const float vmax = fmaxf(vref, fmaxf(vs[0], vs[1]));   // NaN scales are passed over here
-      if (__any_sync(0xffffffffu, move) || vmax > vref) {
-        const float shrink = vmax > 0.f ? vref / vmax : 1.f;
-        vref = vmax;
+      float vratio[2] = {vs[0] * vref.inv, vs[1] * vref.inv}, unit1 = 1.f;     // unit1: of O before the second half
+      if (uneven) {
+        const float unit0 = vref.follow(vs[0]);
+        vratio[0] = vs[0] * vref.inv;
+        unit1 = vref.follow(vs[1]);
+        vratio[1] = vs[1] * vref.inv;
+        if (unit0 != 1.f) scale_o(unit0);
+      }
+      if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           float al[2];
@@ -330,7 +387,7 @@ __global__ void __launch_bounds__(kKbWarps * 32, kv_few_ctas(D, NT)) attn_kv_blo
             const float alpha = mx == m[nt][h] ? 1.f : dec_exp2(m[nt][h] - mx);   // 0 from m = -inf
             m[nt][h] = mx;
             l[nt][h] *= alpha;
-            al[h] = alpha * shrink;
+            al[h] = alpha;
           }
 #pragma unroll
           for (int mt = 0; mt < kChunks; ++mt) {
@@ -341,7 +398,6 @@ __global__ void __launch_bounds__(kKbWarps * 32, kv_few_ctas(D, NT)) attn_kv_blo
           }
         }
       }
-      const float inv_vref = vref > 0.f ? 1.f / vref : 0.f;
       uint32_t pb[2][NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
@@ -350,7 +406,7 @@ __global__ void __launch_bounds__(kKbWarps * 32, kv_few_ctas(D, NT)) attn_kv_blo
         for (int h = 0; h < 2; ++h) mref[h] = (m[nt][h] == -INFINITY ? 0.f : m[nt][h]) - kKbUp;
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const float ratio = vs[u] * inv_vref;
+          const float ratio = vratio[u];
           float p[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -366,7 +422,8 @@ __global__ void __launch_bounds__(kKbWarps * 32, kv_few_ctas(D, NT)) attn_kv_blo
       // O^T += V^T P^T: MMA row g of m-tile mt is dim 16 mt + 2 g, row g + 8 is dim 16 mt + 2 g + 1
       const uint32_t sv = wbuf + st * kStage + kTile + v_row;
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+      for (int u = 0; u < 2; ++u) {
+        if (u == 1 && unit1 != 1.f) scale_o(unit1);
 #pragma unroll
         for (int mp = 0; mp < D / 32; ++mp) {
           uint32_t rr[4];
@@ -380,6 +437,7 @@ __global__ void __launch_bounds__(kKbWarps * 32, kv_few_ctas(D, NT)) attn_kv_blo
             for (int nt = 0; nt < NT; ++nt) mma_f16_16816(o[2 * mp + h][nt], af, pb[u][nt][0], pb[u][nt][1]);
           }
         }
+      }
       __syncwarp();                              // the stage is refilled in the next iteration
       st = st == kKbStages - 1 ? 0 : st + 1;
     }
@@ -408,7 +466,7 @@ __global__ void __launch_bounds__(kKbWarps * 32, kv_few_ctas(D, NT)) attn_kv_blo
     for (int nt = 0; nt < NT; ++nt) {
       float av[2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) av[h] = l[nt][h] == 0.f ? 0.f : vref * (1.f / l[nt][h]);
+      for (int h = 0; h < 2; ++h) av[h] = l[nt][h] == 0.f ? 0.f : vref.v * (1.f / l[nt][h]);
 #pragma unroll
       for (int mt = 0; mt < kChunks; ++mt) {
         float y[4];

@@ -17,6 +17,7 @@ pytestmark = pytest.mark.gpu
 # (heads of the group, tokens): the mma.sync kernel with one and several columns, the
 # tcgen05 kernel with converters, and over tiles converted before the launch
 SHAPES = [(4, 1), (8, 8), (16, 10), (16, 140)]
+FEW = SHAPES[:2]
 
 
 def check_seen(c, q, o, lse, start, count, window=0, n_sink=0):
@@ -100,3 +101,81 @@ def test_largest_scales_stay_finite(kind, G, N, start, alike):
         c.v.copy_(torch.full(c.v.shape, 120.0, device=DEV).to(c.v.dtype))
     q, o, lse = attend(c, G, [start], [N], N, 64, out=torch.float32)
     check_seen(c, q, o, lse, [start], [N])
+
+
+def later(kind, G, N, d, power):
+    """The block of the last tokens has a V scale 2^power larger; the rows before do not see it."""
+    block = 16
+    start = 16 * 13 - max(2, N // 4)
+    c = filled([start + N], block, 1, d, kind)
+    late = sorted({start // block + 1, (start + N - 1) // block})
+    c.v_scale[c.table[0, late].long()] *= 2.0 ** power
+    q, o, lse = attend(c, G, [start], [N], N, d, out=torch.float32)
+    check_seen(c, q, o, lse, [start], [N])
+
+
+def rise_and_fall(kind, G, N, window, n_sink):
+    """V scales from 2^-40 to 2^40 in random order, one of zero, for rows that see some of them."""
+    block, start = 16, 700
+    c = filled([start + N], block, 1, 64, kind, seed=2)
+    row = c.table[0].long()
+    e = torch.randint(-4, 5, (len(row), 1), generator=gen(8), device=DEV)
+    c.v_scale[row] *= torch.exp2(10.0 * e)
+    c.v_scale[row[43]] = 0
+    q, o, lse = attend(c, G, [start], [N], N, 64, window=window, n_sink=n_sink, out=torch.float32)
+    check_seen(c, q, o, lse, [start], [N], window, n_sink)
+
+
+def behind_zero(kind, G, N):
+    """Rows that see blocks of zero scale and small ones; only later rows see large ones."""
+    block = 16
+    start = 16 * 13 - max(2, N // 4)
+    c = filled([start + N], block, 1, 64, kind)
+    row = c.table[0].long()
+    c.v_scale[row] *= 2.0 ** -40
+    c.v_scale[row[:9]] = 0
+    c.v_scale[row[(start + N - 1) // block]] = 1.0
+    q, o, lse = attend(c, G, [start], [N], N, 64, out=torch.float32)
+    check_seen(c, q, o, lse, [start], [N])
+
+
+def no_entry(G, N):
+    """Table entries of blocks that no row sees may be anything."""
+    start, block, window, n_sink = 600, 16, 100, 4
+    c = filled([start + N], block, 1, 64, "int8")
+    q, o, lse = attend(c, G, [start], [N], N, 64, window=window, n_sink=n_sink)
+    c.table[0, unseen_blocks(start, N, block, window, n_sink)] = -1
+    _, o2, lse2 = attend(c, G, [start], [N], N, 64, window=window, n_sink=n_sink)      # device_status() is 0
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+@pytest.mark.parametrize("G,N", FEW)
+@pytest.mark.parametrize("block,start,window,n_sink", UNSEEN)
+@pytest.mark.parametrize("power", [1, 10, 70])
+def test_unseen_scales_of_few_rows(kind, G, N, block, start, window, n_sink, power):
+    unseen(kind, G, N, block, start, window, n_sink, 2.0 ** power)
+
+
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("power", [10, 24, 30, 70])
+def test_later_scales_of_few_rows(kind, d, power):
+    later(kind, 8, 8, d, power)
+
+
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+@pytest.mark.parametrize("G,N", FEW)
+@pytest.mark.parametrize("window,n_sink", [(0, 0), (70, 20)])
+def test_scales_rise_and_fall_for_few_rows(kind, G, N, window, n_sink):
+    rise_and_fall(kind, G, N, window, n_sink)
+
+
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+def test_small_scales_behind_zero_ones_for_few_rows(kind):
+    behind_zero(kind, 8, 8)
+
+
+@pytest.mark.parametrize("G,N", FEW)
+def test_hidden_blocks_of_few_rows_need_no_entry(G, N):
+    no_entry(G, N)
