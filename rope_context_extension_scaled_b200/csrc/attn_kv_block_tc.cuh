@@ -28,9 +28,15 @@
 //    stored in the same order, and O's columns are put back in the epilogue.
 //  * K scales multiply S in the softmax, one factor per 16 columns, inside the
 //    multiply-add that the exponential needs anyway.  V scales go into the fp16
-//    V tile as ratio to the largest met so far (one half-precision product per
-//    pair of codes in the converters, which have the time; 11 bits beside the
-//    8 of a bf16 output); when that grows, O shrinks by the same factor.
+//    V tile as ratio to a reference (one half-precision product per pair of codes
+//    in the converters, which have the time; 11 bits beside the 8 of a bf16
+//    output).  The reference is the largest scale of the keys that the item's rows
+//    see (KIND 2: that any row sees), with some headroom as it grows tile by tile.
+//    16 keys whose scale is below 2^-14 of it take the rest as a power of two 2^lv
+//    that the weights carry (v_part): the row's running reference m is the largest
+//    x + lv, in units of the V reference (so m falls by log2 of its growth), weights
+//    are 2^(x + lv - m), and their sum takes 2^-lv back.  So a row keeps fp16's
+//    range for the scales it sees, whatever the others; lv = 0 nearly always.
 //    A non-finite V scale counts as zero there and marks its 16 keys; a row
 //    that sees a marked key ends as NaN, and no other row does.
 // Converting a tile in every item that sees it is right for few row tiles; the
@@ -72,12 +78,28 @@ constexpr float kBtVUp = KIND == 0 ? 256.f : 32768.f;
 
 struct BtMeta {
   float ks[8];                                  // K scale of each 16 keys
-  uint32_t ratio[8];                            // V scale / vref * kBtVUp, an fp16 pair
-  float vfac;                                   // O's factor before this tile is added
-  uint32_t vbad;                                // 16-key groups with a non-finite V scale
-  float vref;                                   // largest V scale so far
-  uint32_t pad;
+  uint32_t ratio[8];                            // V scale / (vref 2^lv) * kBtVUp, an fp16 pair
+  int8_t lv[8];                                 // of each 16 keys
+  int rare;                                     // kBtWide where a lv is not 0, and the two below; 0 nearly always
+  float vref;                                   // V scales' reference
 };
+
+constexpr int kBtBad = 0xff;                    // 16-key groups with a non-finite V scale
+constexpr int kBtWide = 0x100;
+constexpr int kBtGrown = 16;                    // from this bit on: log2 of vref's growth
+
+// V scale s relative to vref (inv: its inverse): ratio 2^lv, lv = 0 down to a ratio
+// of 2^-14, and 2^-90 at least.  0 for scales that are not finite, and lv = -90 for
+// zero, so that such keys do not raise a row's reference.
+struct VPart {
+  float ratio;
+  int lv;
+};
+__device__ __forceinline__ VPart v_part(float s, float vref, float inv) {
+  if (!(s >= 0x1p-126f && s < INFINITY)) return {0.f, s < 0x1p-126f ? -90 : 0};
+  const int lv = max(-90, min(0, ((__float_as_int(s) - __float_as_int(vref)) >> 23) + 14));
+  return {s * (inv * __int_as_float((127 - lv) << 23)), lv};
+}
 
 // A warp's place in the walk (e, off, x: see SegWalk) and its current segment.
 struct BtSeg {
@@ -185,7 +207,7 @@ static __global__ void __launch_bounds__(256) kv_block_vmax_kernel(const KvAttnA
     const int e = a.c.table[b * a.c.t_sb + j];
     if ((unsigned)e >= (unsigned)a.c.n_blocks) continue;         // reported by the kernels that read it
     const float v = a.c.vs[(int64_t)e * a.c.Hkv + hk];
-    if (v > 0.f && v < INFINITY) m = max(m, __float_as_uint(v));
+    if (v >= 0x1p-126f && v < INFINITY) m = max(m, __float_as_uint(v));
   }
   m = __reduce_max_sync(0xffffffffu, m);
   if (threadIdx.x % 32 == 0) sm[threadIdx.x / 32] = m;
@@ -211,7 +233,7 @@ static __global__ void __launch_bounds__(256) kv_block_expand_kernel(const KvAtt
   if (s.n == 0 || t * kBtN >= hi) return;
   const int lo = a.window > 0 ? max(0, s.start + 1 - a.window) : 0;
   if ((t + 1) * kBtN <= lo && t * kBtN >= min(a.n_sink, lo)) return;
-  const float vref = a.img_vref[(int64_t)bl * kv.Hkv + hk];
+  const float vref = a.img_vref[(int64_t)bl * kv.Hkv + hk], inv = vref > 0.f ? 1.f / vref : 0.f;
   const HiddenBlocks hidden = hidden_blocks(a, s.start);
   uint8_t* img = a.img + (((int64_t)bl * kv.Hkv + hk) * a.img_tiles + t) * 2 * kTile;
 #pragma unroll 4
@@ -228,8 +250,7 @@ static __global__ void __launch_bounds__(256) kv_block_expand_kernel(const KvAtt
         sv = kv.vs[(int64_t)e * kv.Hkv + hk];
       }
     }
-    const float ratio = vref > 0.f && sv > 0.f && sv < INFINITY ? sv / vref * kBtVUp<KIND> : 0.f;
-    const __half2 rh = __float2half2_rn(ratio);
+    const __half2 rh = __float2half2_rn(v_part(sv, vref, inv).ratio * kBtVUp<KIND>);
     const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
     uint32_t h[8], g[8];
 #pragma unroll
@@ -406,12 +427,18 @@ __global__ void __launch_bounds__(kBtThreads, 1) attn_kv_block_tc_kernel(const _
     const uint32_t raw = sbase + L::raw;
     (void)raw;
     int jg = 0, sent[2] = {0, 0};                 // tiles; K and V tiles whose copies were issued
-    // lane i < 8: block of 16-key group i of tile u (0 behind the keys)
+    int hidden = 0;                               // keys up to here, sinks apart, are outside every row's window
+    // whether a row of the item sees one of the 16 keys i = lane % 8 of tile u
+    auto seen = [&](int u, int u1) {
+      const int key = (w->span.tile(u) << kBtLogN) + 16 * (lane & 7);
+      return u < u1 && key < w->span.hi && (key + 15 > hidden || key < a.n_sink);
+    };
+    // lane i < 8: block of 16-key group i of tile u (0 where no row sees it)
     auto load_phys = [&](int u, int u1) {
       int e = 0;
       if (u < u1) {
         const int key = (w->span.tile(u) << kBtLogN) + 16 * (lane & 7);
-        if (key < w->span.hi) {
+        if (seen(u, u1)) {
           e = kv.table[(int64_t)w->b * kv.t_sb + (key >> lb)];
           if ((unsigned)e >= (unsigned)kv.n_blocks) {
             record_device_error(RCX_ERR_DEVICE_INDEX);
@@ -424,7 +451,7 @@ __global__ void __launch_bounds__(kBtThreads, 1) attn_kv_block_tc_kernel(const _
     // lanes 0-7 K, 8-15 V scale of the groups of tile u with blocks ph
     auto load_scale = [&](int u, int u1, int ph) {
       float sc = 0.f;
-      if (u < u1 && lane < 16 && (w->span.tile(u) << kBtLogN) + 16 * (lane & 7) < w->span.hi)
+      if (lane < 16 && seen(u, u1))
         sc = (lane < 8 ? kv.ks : kv.vs)[(int64_t)ph * kv.Hkv + w->hk];
       return sc;
     };
@@ -469,35 +496,58 @@ __global__ void __launch_bounds__(kBtThreads, 1) attn_kv_block_tc_kernel(const _
     };
     while (ok && bt_next(w, a, lane)) {
       const int u0 = w->u0, u1 = u0 + w->n;
+      hidden = a.window > 0 ? w->start + (int)fast_div(w->r0, a.div_g) - a.window : -1;
       int ph = load_phys(u0, u1), ph_next = load_phys(u0 + 1, u1);
       float sc = load_scale(u0, u1, ph);
-      float vref = 0.f;
+      float vref = 0.f, inv = 0.f;
+      if constexpr (KIND == 2) {
+        vref = a.img_vref[(int64_t)(w->b - a.b0) * kv.Hkv + w->hk];
+        inv = vref > 0.f ? 1.f / vref : 0.f;
+      }
       for (int u = u0; u < u1; ++u, ++jg) {
         const int ph_next2 = load_phys(u + 2, u1);
         const float sc_next = load_scale(u + 1, u1, ph_next);
         if (!(ok = wait_place(0))) break;
         copy_codes(u, ph, 0);
-        // V scales: running maximum, ratios in fp16 (lanes 8-15 hold the groups')
+        // V scales (lanes 8-15 hold the groups'): the first one that is not zero times a
+        // power of two is their reference, at least twice the largest where it begins or
+        // grows, so that it seldom does
         const bool is_v = lane >= 8 && lane < 16;
         const bool bad = is_v && !(fabsf(sc) < INFINITY);
-        const float sv = is_v && !bad ? sc : 0.f;
-        const float vmax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(sv, 0.f))));
         const uint32_t vbad = (__ballot_sync(0xffffffffu, bad) >> 8) & 0xffu;
-        const float vnew = KIND == 2 ? a.img_vref[(int64_t)(w->b - a.b0) * kv.Hkv + w->hk] : fmaxf(vref, vmax);
-        const float ratio = vnew > 0.f ? sv / vnew * kBtVUp<KIND> : 0.f;
+        int grown = 0;
+        if constexpr (KIND != 2) {
+          const bool counts = is_v && !bad && sc >= 0x1p-126f;
+          const int top = (int)__reduce_max_sync(0xffffffffu, counts ? __float_as_uint(sc) : 0u);
+          if (top > __float_as_int(vref)) {
+            const bool first = vref == 0.f;
+            if (first) {
+              vref = __shfl_sync(0xffffffffu, sc, __ffs(__ballot_sync(0xffffffffu, counts)) - 1);
+              inv = 1.f / vref;
+            }
+            const int k = max(0, min(((top - __float_as_int(vref) + 0x7fffff) >> 23) + 1, 251 - (__float_as_int(vref) >> 23)));
+            vref = __int_as_float(__float_as_int(vref) + (k << 23));
+            inv = __int_as_float(__float_as_int(inv) - (k << 23));
+            grown = first ? 0 : k;               // (nothing but zeros so far: O is 0)
+          }
+        }
+        VPart part = v_part(sc, vref, inv);
+        if (!is_v || !seen(u, u1)) part = {0.f, 0};
+        const bool wide = __any_sync(0xffffffffu, part.lv != 0);
         // the slot's last reader was the softmax of tile jg - 8: the copies above waited
         // for K of jg - 1 to be read, so K of jg - 2 stands in its stage and S of jg - 4
         // is done, which came after both slots' weights of jg - 5 (KIND 2: for S of
         // jg - 2, after their weights of jg - 3)
         BtMeta* mt = meta + jg % kBtMeta;
         if (lane < 8) mt->ks[lane] = sc;
-        if (is_v) mt->ratio[lane - 8] = f2_to_h2(ratio, ratio);
-        if (lane == 0) {
-          mt->vfac = KIND != 2 && vnew > 0.f ? vref / vnew : 1.f;
-          mt->vbad = vbad;
-          mt->vref = vnew;
+        if (is_v) {
+          mt->ratio[lane - 8] = f2_to_h2(part.ratio * kBtVUp<KIND>, part.ratio * kBtVUp<KIND>);
+          mt->lv[lane - 8] = (int8_t)part.lv;
         }
-        vref = vnew;
+        if (lane == 0) {
+          mt->rare = (grown << kBtGrown) | (wide ? kBtWide : 0) | (int)vbad;
+          mt->vref = vref;
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(BAR(B_META + jg % kBtMeta));
         if (!(ok = wait_place(1))) break;
@@ -708,11 +758,28 @@ __global__ void __launch_bounds__(kBtThreads, 1) attn_kv_block_tc_kernel(const _
               if (c > lim || (c <= win_lo && c > snk)) x[c] = -INFINITY;
           }
         }
-        if (mt->vbad) {                         // NaN for the rows that see a marked key
-          for (int c = 0; c < kBtN; ++c)
-            if (((mt->vbad >> (c >> 4)) & 1) && key0 + c <= gi &&
-                (a.window == 0 || key0 + c > gi - a.window || key0 + c < a.n_sink))
-              poison = __uint_as_float(0x7fffffffu);
+        float of = 1.f;                         // O's factor
+        const int rare = mt->rare;
+        if (__builtin_expect(rare != 0, 0)) {
+          if (rare & kBtBad) {                  // NaN for the rows that see a marked key
+            for (int c = 0; c < kBtN; ++c)
+              if (((rare >> (c >> 4)) & 1) && key0 + c <= gi &&
+                  (a.window == 0 || key0 + c > gi - a.window || key0 + c < a.n_sink))
+                poison = __uint_as_float(0x7fffffffu);
+          }
+          if (rare & kBtWide) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              const float e = (float)mt->lv[q];
+#pragma unroll
+              for (int c = 16 * q; c < 16 * q + 16; ++c) x[c] += e;
+            }
+          }
+          // m in units of the new reference; where l would pass 2^96, O takes the rest
+          const int by = rare >> kBtGrown, sh = max(0, min(by, 96 + 127 - (int)(__float_as_uint(l) >> 23)));
+          m_used -= (float)sh;
+          if (l > 0.f) l *= __int_as_float((127 + sh) << 23);
+          of = by - sh > 126 ? 0.f : __int_as_float((127 - by + sh) << 23);
         }
         float m8[8];
 #pragma unroll
@@ -725,7 +792,6 @@ __global__ void __launch_bounds__(kBtThreads, 1) attn_kv_block_tc_kernel(const _
         const float mx = fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7]));
         const float m_new = fmaxf(m_used, mx);
         const bool need = m_new > m_used + kLazyRescale;
-        float of = mt->vfac;                    // O's factor
         vref = mt->vref;
         if (need) {
           const float alpha = fast_exp2(m_used - m_new);   // 0 when m_used = -inf
@@ -736,6 +802,15 @@ __global__ void __launch_bounds__(kBtThreads, 1) attn_kv_block_tc_kernel(const _
         const float mref = kKbUp - (m_used == -INFINITY ? 0.f : m_used);
         // weights, packed in pairs, over the columns of S as they are made
         float l2[2] = {0.f, 0.f};
+        if (__builtin_expect(rare & kBtWide, 0)) {   // l's terms, without 2^lv
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            float t = 0.f;
+#pragma unroll
+            for (int c = 16 * q; c < 16 * q + 16; ++c) t += fast_exp2(x[c] + mref);
+            l += t * __int_as_float((127 - mt->lv[q]) << 23);
+          }
+        }
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           uint32_t pc[16];
@@ -750,7 +825,7 @@ __global__ void __launch_bounds__(kBtThreads, 1) attn_kv_block_tc_kernel(const _
           }
           tmem_st16(tS(s) + lane_off + 16 * q, pc);
         }
-        l += l2[0] + l2[1];
+        if (!(rare & kBtWide)) l += l2[0] + l2[1];
         if (__any_sync(0xffffffffu, of != 1.f) && j > 0) {
 #pragma unroll 1
           for (int cb = 0; cb < D / 32; ++cb) {

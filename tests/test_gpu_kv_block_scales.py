@@ -17,7 +17,7 @@ pytestmark = pytest.mark.gpu
 # (heads of the group, tokens): the mma.sync kernel with one and several columns, the
 # tcgen05 kernel with converters, and over tiles converted before the launch
 SHAPES = [(4, 1), (8, 8), (16, 10), (16, 140)]
-FEW = SHAPES[:2]
+FEW, MANY = SHAPES[:2], SHAPES[2:]
 
 
 def check_seen(c, q, o, lse, start, count, window=0, n_sink=0):
@@ -178,4 +178,51 @@ def test_small_scales_behind_zero_ones_for_few_rows(kind):
 
 @pytest.mark.parametrize("G,N", FEW)
 def test_hidden_blocks_of_few_rows_need_no_entry(G, N):
+    no_entry(G, N)
+
+
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+@pytest.mark.parametrize("block,start,window,n_sink", UNSEEN)
+@pytest.mark.parametrize("power", [1, 10, 70])
+def test_unseen_scales_of_many_rows(kind, block, start, window, n_sink, power):
+    unseen(kind, 16, 10, block, start, window, n_sink, 2.0 ** power)
+
+
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+@pytest.mark.parametrize("G,N", MANY)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("power", [10, 24, 30, 70])
+def test_later_scales_of_many_rows(kind, G, N, d, power):
+    later(kind, G, N, d, power)
+
+
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+@pytest.mark.parametrize("G,N", MANY + [(16, 60)])
+@pytest.mark.parametrize("window,n_sink", [(0, 0), (70, 20)])
+def test_scales_rise_and_fall_for_many_rows(kind, G, N, window, n_sink):
+    rise_and_fall(kind, G, N, window, n_sink)
+
+
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+@pytest.mark.parametrize("G,N", MANY)
+def test_small_scales_behind_zero_ones_for_many_rows(kind, G, N):
+    behind_zero(kind, G, N)
+
+
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+@pytest.mark.parametrize("G,N", [(16, 100), (16, 140)])
+@pytest.mark.parametrize("power", [8, 40, 100])
+def test_scales_that_grow_along_the_keys(kind, G, N, power):
+    """From 2^-power to 2^power over 2000 tokens, the causal border inside the last tiles: the
+    reference grows many times, and early rows see none of the last blocks."""
+    block, start = 16, 2000
+    c = filled([start + N], block, 1, 64, kind)
+    row = c.table[0].long()
+    c.v_scale[row] *= torch.exp2(torch.linspace(-power, power, len(row), device=DEV).round())[:, None]
+    q, o, lse = attend(c, G, [start], [N], N, 64, out=torch.float32)
+    check_seen(c, q, o, lse, [start], [N])
+
+
+@pytest.mark.parametrize("G,N", MANY)
+def test_hidden_blocks_of_many_rows_need_no_entry(G, N):
     no_entry(G, N)
