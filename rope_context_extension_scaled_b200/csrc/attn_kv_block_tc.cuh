@@ -204,8 +204,8 @@ static __global__ void __launch_bounds__(256) kv_block_vmax_kernel(const KvAttnA
 #pragma unroll 4
   for (int j = threadIdx.x; j < blocks; j += 256) {
     if (hidden.has(j)) continue;
-    const int e = a.c.table[b * a.c.t_sb + j];
-    if ((unsigned)e >= (unsigned)a.c.n_blocks) continue;         // reported by the kernels that read it
+    int e = a.c.table[b * a.c.t_sb + j];
+    if ((unsigned)e >= (unsigned)a.c.n_blocks) e = 0;            // reported by the kernels that read it
     const float v = a.c.vs[(int64_t)e * a.c.Hkv + hk];
     if (v >= 0x1p-126f && v < INFINITY) m = max(m, __float_as_uint(v));
   }
@@ -242,13 +242,11 @@ static __global__ void __launch_bounds__(256) kv_block_expand_kernel(const KvAtt
     uint4 x = make_uint4(0u, 0u, 0u, 0u), y = x;
     float sv = 0.f;
     if (key < hi && !hidden.has(key >> kv.block_log2)) {
-      const int e = checked_block(kv, b, key >> kv.block_log2);
+      const int e = max(0, checked_block(kv, b, key >> kv.block_log2));      // a bad entry reads as block 0
       const int64_t r = key & ((1 << kv.block_log2) - 1);
-      if (e >= 0) {
-        x = __ldcs(reinterpret_cast<const uint4*>(kv.k + e * kv.k_sb + r * kv.k_sn + hk * kv.k_sh + pc * 16));
-        y = __ldcs(reinterpret_cast<const uint4*>(kv.v + e * kv.v_sb + r * kv.v_sn + hk * kv.v_sh + pc * 16));
-        sv = kv.vs[(int64_t)e * kv.Hkv + hk];
-      }
+      x = __ldcs(reinterpret_cast<const uint4*>(kv.k + e * kv.k_sb + r * kv.k_sn + hk * kv.k_sh + pc * 16));
+      y = __ldcs(reinterpret_cast<const uint4*>(kv.v + e * kv.v_sb + r * kv.v_sn + hk * kv.v_sh + pc * 16));
+      sv = kv.vs[(int64_t)e * kv.Hkv + hk];
     }
     const __half2 rh = __float2half2_rn(v_part(sv, vref, inv).ratio * kBtVUp<KIND>);
     const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};

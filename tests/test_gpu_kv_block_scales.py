@@ -226,3 +226,19 @@ def test_scales_that_grow_along_the_keys(kind, G, N, power):
 @pytest.mark.parametrize("G,N", MANY)
 def test_hidden_blocks_of_many_rows_need_no_entry(G, N):
     no_entry(G, N)
+
+
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+@pytest.mark.parametrize("G,N", SHAPES)
+def test_a_bad_block_number_reads_as_block_0(kind, G, N):
+    start, block = 300, 32
+    c = filled([start + N], block, 1, 64, kind)
+    q = torch.randn(1, N, G, 64, generator=gen(5), device=DEV).to(torch.bfloat16)
+    c.table[0, 3] = 0
+    want = _lib.attn_kv_block_fwd(q, c, lens_of([start]))
+    assert _lib.device_status() == 0
+    for bad in (-7, c.k.shape[0], 2 ** 31 - 1):
+        c.table[0, 3] = bad
+        o, lse = _lib.attn_kv_block_fwd(q, c, lens_of([start]))
+        assert _lib.device_status() == _lib.RCX_ERR_DEVICE_INDEX
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
