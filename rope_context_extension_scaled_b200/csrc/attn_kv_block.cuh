@@ -258,7 +258,8 @@ __global__ void __launch_bounds__(kKbWarps * 32, kv_few_ctas(D, NT)) attn_kv_blo
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[mt][nt][e] = 0.f;
     VRef vref = {0.f, 0.f, 0.f};
-    bool uneven = false;                         // the reference moves tile by tile
+    bool uneven = false;                         // the reference moves tile by tile, or a scale is NaN
+    uint32_t poison = 0;                         // rows 8 nt + 2 c + h (bit 2 nt + h) that saw one
     auto scale_o = [&](float f) {
 #pragma unroll
       for (int mt = 0; mt < kChunks; ++mt)
@@ -281,7 +282,7 @@ __global__ void __launch_bounds__(kKbWarps * 32, kv_few_ctas(D, NT)) attn_kv_blo
         const uint32_t bits = vs_a > 0.f ? __float_as_uint(vs_a) : 0u;
         const float hi = __uint_as_float(__reduce_max_sync(0xffffffffu, bits));
         const float lo = __uint_as_float(__reduce_min_sync(0xffffffffu, bits ? bits : 0x7f7fffffu));
-        uneven = hi > 0.f && lo * 16.f < hi;
+        uneven = (hi > 0.f && lo * 16.f < hi) || __any_sync(0xffffffffu, vs_a != vs_a);
         if (hi > 0.f && !uneven) {
           vref.begin(__shfl_sync(0xffffffffu, vs_a, __ffs(__ballot_sync(0xffffffffu, bits != 0u)) - 1));
           if (!vref.holds(lo, hi)) scale_o(vref.move(hi));
@@ -372,6 +373,17 @@ __global__ void __launch_bounds__(kKbWarps * 32, kv_few_ctas(D, NT)) attn_kv_blo
         unit1 = vref.follow(vs[1]);
         vratio[1] = vs[1] * vref.inv;
         if (unit0 != 1.f) scale_o(unit0);
+        // a block of scale NaN makes NaN of the rows that see it, however small their weight, and only of those
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          if (vs[u] != vs[u]) {
+            vratio[u] = 0.f;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (s[u][nt][e] != -INFINITY) poison |= 1u << (2 * nt + (e & 1));
+          }
       }
       if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
@@ -412,8 +424,7 @@ __global__ void __launch_bounds__(kKbWarps * 32, kv_few_ctas(D, NT)) attn_kv_blo
           for (int e = 0; e < 4; ++e) {
             p[e] = dec_exp2(s[u][nt][e] - mref[e & 1]);
             l[nt][e & 1] += p[e];
-            // a weight of zero takes nothing, not even NaN, from its block
-            p[e] = p[e] == 0.f ? 0.f : p[e] * ratio;
+            p[e] *= ratio;
           }
           pb[u][nt][0] = movmatrix_t(f2_to_h2(p[0], p[1]));   // keys 2c, 2c + 1 of row 8 nt + g
           pb[u][nt][1] = movmatrix_t(f2_to_h2(p[2], p[3]));   // keys 2c + 8, 2c + 9
@@ -456,6 +467,8 @@ __global__ void __launch_bounds__(kKbWarps * 32, kv_few_ctas(D, NT)) attn_kv_blo
           sm_l[warp][8 * nt + 2 * c + h] = l[nt][h];
         }
       }
+#pragma unroll
+    for (int i = 4; i < 32; i *= 2) poison |= __shfl_xor_sync(0xffffffffu, poison, i);
     __syncthreads();
     // [warps][8 NT][D + 4]: the pad spreads the rows of a store over the banks
     float* sm_o = reinterpret_cast<float*>(kb_smem);
@@ -466,7 +479,8 @@ __global__ void __launch_bounds__(kKbWarps * 32, kv_few_ctas(D, NT)) attn_kv_blo
     for (int nt = 0; nt < NT; ++nt) {
       float av[2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) av[h] = l[nt][h] == 0.f ? 0.f : vref.v * (1.f / l[nt][h]);
+      for (int h = 0; h < 2; ++h)
+        av[h] = (poison >> (2 * nt + h)) & 1u ? __uint_as_float(0x7fffffffu) : l[nt][h] == 0.f ? 0.f : vref.v * (1.f / l[nt][h]);
 #pragma unroll
       for (int mt = 0; mt < kChunks; ++mt) {
         float y[4];
@@ -593,6 +607,7 @@ static __global__ void __launch_bounds__(256) attn_kv_block_merge_kernel(const K
         // (even: an item with fewer tiles than pieces leaves some without any)
         const bool there = lane < n && (even == 0 || nt >= even || range_start(nt, c - c0, even) < range_start(nt, c - c0 + 1, even));
         const float ls = there ? a.part_lse[pr] : -INFINITY;
+        const uint32_t some = __ballot_sync(0xffffffffu, ls != -INFINITY);       // partials with keys, however small
         float mn = ls;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));   // passes NaN over
@@ -612,7 +627,7 @@ static __global__ void __launch_bounds__(256) attn_kv_block_merge_kernel(const K
         for (int i = 0; i < n; ++i) {
           const float wi = __shfl_sync(0xffffffffu, wt, i);
           const int64_t pi = __shfl_sync(0xffffffffu, pr, i);
-          if (wi == 0.f) continue;
+          if (!((some >> i) & 1u)) continue;
           const float4 y = *reinterpret_cast<const float4*>(a.part_o + pi * D + dd);
           x.x += wi * y.x; x.y += wi * y.y; x.z += wi * y.z; x.w += wi * y.w;
         }

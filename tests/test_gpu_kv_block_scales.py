@@ -242,3 +242,22 @@ def test_a_bad_block_number_reads_as_block_0(kind, G, N):
         o, lse = _lib.attn_kv_block_fwd(q, c, lens_of([start]))
         assert _lib.device_status() == _lib.RCX_ERR_DEVICE_INDEX
         assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.parametrize("G,N", SHAPES)
+@pytest.mark.parametrize("start", [100, 9000])
+def test_nan_scale_reaches_rows_that_give_it_no_weight(G, N, start):
+    """A visible block of V scale NaN makes NaN, however small its weight (start = 9000:
+    more partials than one warp of the merge loads at once)."""
+    block, d = 16, 64
+    c = filled([start + N], block, 1, d, "int8")
+    q = torch.ones(1, N, G, d, dtype=torch.bfloat16, device=DEV)
+    c.k.fill_(1)
+    p = int(c.table[0, 2])
+    c.k[c.table[0, :20].long() if start > 1000 else p] = -127  # logits 1024 below the others
+    c.k_scale.fill_(1.0)
+    o, lse = _lib.attn_kv_block_fwd(q, c, lens_of([start]))
+    assert torch.isfinite(o.float()).all()
+    c.v_scale[p] = float("nan")
+    o2, lse2 = _lib.attn_kv_block_fwd(q, c, lens_of([start]))
+    assert torch.isnan(o2).all() and torch.equal(lse, lse2)
