@@ -156,9 +156,8 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 }
 
 // Packed fp32 arithmetic: two values an instruction.
-// (volatile: the first use of values from tcgen05.ld must stay behind its wait)
 __device__ __forceinline__ void mul2(float& a, float& b, float f) {
-  asm volatile("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %2};\n\t"
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %2};\n\t"
       "mul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
       : "+f"(a), "+f"(b)
       : "f"(f));
@@ -687,7 +686,7 @@ __global__ void __launch_bounds__(kBtThreads, 1) attn_kv_block_tc_kernel(const _
         for (int cb = 0; cb < D / 32; ++cb) {
           uint32_t o[32];
           tmem_ld32(tO(s) + lane_off + cb * 32, o);
-          tmem_wait_ld();
+          tmem_wait_ld<32>(o);
           if (row_ok) {
             float y[32];
 #pragma unroll
@@ -734,7 +733,7 @@ __global__ void __launch_bounds__(kBtThreads, 1) attn_kv_block_tc_kernel(const _
         const BtMeta* mt = meta + g % kBtMeta;
         const int key0 = w->span.tile(w->u0 + j) << kBtLogN;
         const bool full = (key0 <= full_hi) && (key0 > full_lo || key0 + kBtN <= a.n_sink);
-        tmem_wait_ld();
+        tmem_wait_ld<128>(reinterpret_cast<uint32_t*>(x));
         // logits in log2 units: the product is rounded here, once, so that the row
         // maximum below is one of them and the winner's weight is 2^0 exactly
 #pragma unroll
@@ -829,7 +828,7 @@ __global__ void __launch_bounds__(kBtThreads, 1) attn_kv_block_tc_kernel(const _
           for (int cb = 0; cb < D / 32; ++cb) {
             uint32_t o[32];
             tmem_ld32(tO(s) + lane_off + cb * 32, o);
-            tmem_wait_ld();
+            tmem_wait_ld<32>(o);
 #pragma unroll
             for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * of);
             tmem_st32(tO(s) + lane_off + cb * 32, o);

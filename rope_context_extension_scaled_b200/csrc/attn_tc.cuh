@@ -270,7 +270,17 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
       : "memory");
 }
 
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// Waits for the tcgen05.ld of r[0 .. N).  The empty statements behind the wait
+// write those registers as the compiler sees it, so arithmetic on them cannot be
+// moved before it.
+template <int N>
+__device__ __forceinline__ void tmem_wait_ld(uint32_t* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < N; i += 8)
+    asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
+                 "+r"(r[i + 6]), "+r"(r[i + 7]));
+}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // max of three floats in one instruction
@@ -737,7 +747,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tmem_ld32(tS[s] + lane_off + 32, sr + 32);
         tmem_ld32(tS[s] + lane_off + 64, sr + 64);
         tmem_ld32(tS[s] + lane_off + 96, sr + 96);
-        tmem_wait_ld();
+        tmem_wait_ld<128>(sr);
         const int j0 = (int)a.k_start + tile * kTcBN;
         const bool full = (j0 + kTcBN <= key_end) &&
                           tile_all_visible(ti_lo, ti_hi, j0, j0 + kTcBN - 1, a.window, a.n_sink);
@@ -798,7 +808,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           for (int cb = 0; cb < 4; ++cb) {
             uint32_t o[32];
             tmem_ld32(tO[s] + lane_off + cb * 32, o);
-            tmem_wait_ld();
+            tmem_wait_ld<32>(o);
 #pragma unroll
             for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
             tmem_st32(tO[s] + lane_off + cb * 32, o);
@@ -843,7 +853,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         uint32_t o[32];
         if (n > 0) {
           tmem_ld32(tO[s] + lane_off + cbk * 32, o);
-          tmem_wait_ld();
+          tmem_wait_ld<32>(o);
         } else {
 #pragma unroll
           for (int c = 0; c < 32; ++c) o[c] = 0u;
