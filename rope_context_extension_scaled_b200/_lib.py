@@ -234,6 +234,9 @@ def rope_apply(q, k, inv_freq, positions=None, q_out=None, k_out=None):
     st = load().rcx_rope_apply(view(q), view(k), view(q_out if q is not None else None),
                                view(k_out if k is not None else None), pp, npos, fp, _stream(dev))
     _check(st, "rcx_rope_apply")
+    for x, y in ((q, q_out), (k, k_out)):
+        if x is not None and not y.is_inference():
+            torch.autograd.graph.increment_version(y)      # autograd sees that y has changed
     return q_out, k_out
 
 
@@ -471,7 +474,9 @@ def rope_axes_apply(q, k, inv_freq, axis, positions, halves=False, inverse=False
 
     Pair i turns by positions[axis[i], b, n] * inv_freq[i]; the pair is (i, i + d/2)
     with halves, else (2i, 2i + 1); inverse turns back, which is the gradient of
-    the rotation (no autograd graph is recorded).  inv_freq [d/2] and axis [d/2]
+    the rotation.  No autograd graph is recorded; an output that requires grad is
+    refused while gradients are recorded, and a tensor that autograd has saved counts
+    as changed when it is written.  inv_freq [d/2] and axis [d/2]
     are host arrays, positions an int64 [axes, B, N] tensor (axis and batch
     strides are free, 0 included).  Default: in place."""
     if q is None and k is None:

@@ -10,6 +10,7 @@
 // returned for the Python side to raise.
 #include <torch/csrc/autograd/python_variable.h>
 #include <ATen/ATen.h>
+#include <ATen/core/grad_mode.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
@@ -38,6 +39,21 @@ long long integer(PyObject* x) {
   const long long v = PyLong_AsLongLong(x);
   if (v == -1 && PyErr_Occurred()) throw PyError();
   return v;
+}
+
+// Before a call writes t behind autograd's back: refuses what torch's own in-place
+// operations refuse, a tensor that gradients are wanted of.
+void check_output(const at::Tensor* t, const char* name) {
+  if (t && t->requires_grad() && at::GradMode::is_enabled()) {
+    PyErr_Format(PyExc_ValueError, "%s would be written in place, but it requires grad: pass another output, or call under "
+                                   "torch.no_grad()", name);
+    throw PyError();
+  }
+}
+
+// After the write: autograd then sees that what it saved has changed.
+void written(const at::Tensor* t) {
+  if (t && !t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
 }
 
 rcx_tensor null_view() {
@@ -173,11 +189,18 @@ PyObject* rope_axes_apply(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (k) dev.add(ko);
     const rcx_tensor tqo = q ? view4(*qo) : null_view(), tko = k ? view4(*ko) : null_view();
     const long long flags = integer(a[7]);
+    check_output(q ? qo : nullptr, "q_out");
+    check_output(k ? ko : nullptr, "k_out");
     OnDevice on(dev.index);
-    return PyLong_FromLong(rcx_rope_axes_apply(
+    const int st = rcx_rope_axes_apply(
         tq, tk, tqo, tko, pos->data_ptr<int64_t>(), (int)std::min<int64_t>(pos->size(0), 1 << 20), pos->stride(0),
         pos->stride(1), static_cast<const double*>(inv.b.buf), static_cast<const int32_t*>(axis.b.buf), (int)flags,
-        on.stream));
+        on.stream);
+    if (st == RCX_OK) {
+      written(q ? qo : nullptr);
+      written(k ? ko : nullptr);
+    }
+    return PyLong_FromLong(st);
   });
 }
 
@@ -210,6 +233,7 @@ PyObject* kv_block_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
       const at::Tensor* given = tensor(a[5 + i], "output", true);
       if (given) {
         dev.add(given);
+        check_output(given, i ? "v_out" : "k_out");
         out[i] = *given;
       } else {
         out[i] = at::empty({B, len, pool->size(2), pool->size(3)},
@@ -220,6 +244,8 @@ PyObject* kv_block_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t* lengths = per_sequence(a[3], "lengths", B, dev);
     OnDevice on(dev.index);
     const int st = rcx_kv_block_read(blocks(a[1]), lengths, view4(out[0]), view4(out[1]), on.stream);
+    for (int i = 0; i < 2; ++i)
+      if (st == RCX_OK && a[5 + i] != Py_None) written(&out[i]);
     return Py_BuildValue("iNN", st, THPVariable_Wrap(out[0]), THPVariable_Wrap(out[1]));
   });
 }
@@ -245,6 +271,8 @@ PyObject* attn_kv_block_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (t == -1.0 && PyErr_Occurred()) throw PyError();
     const int want_lse = PyObject_IsTrue(a[11]);
     if (want_lse < 0) throw PyError();
+    check_output(o_in, "o");
+    check_output(lse_in, "lse");
     OnDevice on(dev.index);
     const at::Tensor o = o_in ? *o_in : at::empty(q->sizes(), q->options());
     at::Tensor lse, ws;
@@ -259,6 +287,10 @@ PyObject* attn_kv_block_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     const int st = rcx_attn_kv_block_fwd(tq, cache, start, count, view4(o), lse.defined() ? lse_view(lse) : null_view(),
                                          window, n_sink, t, ws.data_ptr(), (int64_t)ws.nbytes(), on.stream);
+    if (st == RCX_OK) {
+      written(o_in);
+      written(lse_in);
+    }
     PyObject* l = lse.defined() ? THPVariable_Wrap(lse) : Py_NewRef(Py_None);
     return Py_BuildValue("iNN", st, THPVariable_Wrap(o), l);
   });
