@@ -21,6 +21,7 @@ OBJ = os.path.join(PKG, "_build")
 OUT = os.path.join(PKG, "librcx.so")
 EXT_SRC = os.path.join(CSRC, "torch_binding.cpp")
 EXT = os.path.join(PKG, "_rcx_torch.so")
+EXT_ABI = os.path.join(OBJ, "_rcx_torch.abi")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = [
@@ -54,10 +55,23 @@ def up_to_date() -> bool:
     return _newest(units() + headers() + [os.path.abspath(__file__)]) <= os.path.getmtime(OUT)
 
 
+def ext_abi() -> str:
+    """What _rcx_torch.so is built against: another torch, Python or C++ ABI needs another build."""
+    import torch
+    return f"torch {torch.__version__}, cxx11 {int(torch._C._GLIBCXX_USE_CXX11_ABI)}, python {sys.version}"
+
+
+def ext_up_to_date() -> bool:
+    deps = [EXT_SRC, os.path.join(ROOT, "include", "rcx.h"), os.path.abspath(__file__)]
+    if not os.path.exists(EXT) or not os.path.exists(EXT_ABI) or _newest(deps) > os.path.getmtime(EXT):
+        return False
+    with open(EXT_ABI) as f:
+        return f.read() == ext_abi()
+
+
 def build_ext(force: bool = False) -> str:
     """Compile _rcx_torch.so against the installed torch (librcx.so has to be there)."""
-    deps = [EXT_SRC, os.path.join(ROOT, "include", "rcx.h"), os.path.abspath(__file__)]
-    if not force and os.path.exists(EXT) and _newest(deps) <= os.path.getmtime(EXT):
+    if not force and ext_up_to_date():
         return EXT
     import sysconfig
 
@@ -73,6 +87,9 @@ def build_ext(force: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError("torch_binding.cpp failed:\n" + r.stdout + r.stderr)
     os.replace(EXT + ".tmp", EXT)
+    os.makedirs(OBJ, exist_ok=True)
+    with open(EXT_ABI, "w") as f:
+        f.write(ext_abi())
     return EXT
 
 
