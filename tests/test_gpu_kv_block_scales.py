@@ -261,3 +261,21 @@ def test_nan_scale_reaches_rows_that_give_it_no_weight(G, N, start):
     c.v_scale[p] = float("nan")
     o2, lse2 = _lib.attn_kv_block_fwd(q, c, lens_of([start]))
     assert torch.isnan(o2).all() and torch.equal(lse, lse2)
+
+
+# ------------------------------------------------------------------ tables with room for more
+
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+@pytest.mark.parametrize("capacity", [1 << 20, (1 << 21) + 5000])
+def test_many_rows_in_wide_tables(kind, capacity):
+    """2240 rows where a table row has room for 1M tokens (the converted tiles of one
+    sequence at a time fit the workspace) and for more than 2M (they do not fit)."""
+    block, start, N, G = 128, [500, 90, 0], 140, 16
+    c = filled([s + N for s in start], block, 1, 128, kind)
+    table = torch.full((3, capacity // block), -1, dtype=torch.int32, device=DEV)
+    table[:, :c.table.shape[1]] = c.table
+    wide = _lib.KvBlockCache(c.k, c.v, c.k_scale, c.v_scale, table)
+    count = [N, N - 1, N]
+    for window, n_sink in ((0, 0), (130, 3)):
+        q, o, lse = attend(wide, G, start, count, N, 128, window=window, n_sink=n_sink)
+        check_seen(c, q, o, lse, start, count, window, n_sink)
