@@ -310,15 +310,18 @@ int rcx_attn_decode_int8_fwd(rcx_tensor q, rcx_tensor k, const float* k_scale, r
  * for both); block 16, 32, 64 or 128; d 64 or 128; stride[3] == 1, base pointers
  * and the other strides multiples of 16 bytes (the layout may be
  * [n_blocks, Hkv, block, d] underneath).  k_scale, v_scale: device fp32
- * [n_blocks, Hkv], contiguous, never negative.  table: device int32 [B, width];
- * entries of blocks that hold no token of the sequence are not read.
+ * [n_blocks, Hkv], contiguous, never negative (below 2^-126 attention takes a V
+ * scale as 0).  table: device int32 [B, width]; entries of blocks that hold no token
+ * of the sequence are not read, nor, by attention, those that the window hides from
+ * every row.
  *
  * Scale and code of a block whose largest |x| is amax (0: scale 0, codes 0):
  *   RCX_I8:   s = fl(amax / 127), at least 2^-120; code = rint(x * fl(1 / s)),
  *             the product unrounded, ties to even
  *   RCX_E4M3: s = the smallest power of two with amax <= 448 s (2^-120 ..
  *             2^120); code = e4m3(x / s), ties to even
- * A block given an infinity or NaN gets scale NaN: its tokens read back as NaN.
+ * A block given an infinity or NaN gets scale NaN: its tokens read back as NaN, and
+ * so does the attention of every row that sees one of them, however small its weight.
  * The NaN codes of RCX_E4M3 are never written; readers take them as +-480.
  *
  * Lengths and block numbers are device data, so their errors show on the device:
@@ -375,11 +378,18 @@ int rcx_kv_block_read(const rcx_kv_blocks* cache, const int64_t* len, rcx_tensor
  * q: [B, N, Hq, d] bf16, already rotated, 16-byte aligned base and strides; any
  * Hq that is a multiple of Hkv; o: same shape, bf16 (8-byte aligned) or f32
  * (16-byte); lse: [B, Hq, N, 1] fp32 or ptr NULL.  start, count as for append.
- * The logits are fp32 sums of exact products of q and the codes; softmax
- * weights enter the product with V in fp16 with fp32 sums.  Up to 64 rows
- * (N * Hq / Hkv) run on mma.sync and read each code once; more run on tcgen05
- * (the workspace of 2048 and more then holds an fp16 copy of the cached tokens
- * that a table row has room for, where that is at most 1 GiB a sequence).
+ * The logits are fp32 sums of exact products of q and the codes.  Softmax weights
+ * enter the product with V in fp16 (11 bits, down to 2^-28 of the largest), and so
+ * does, on tcgen05, V itself (code times V scale, two roundings); sums are fp32.  O
+ * is off by about 2^-10 of the largest |v| that a row sees, also where o is f32;
+ * V scales that the row does not see have no part in that while they are within
+ * 2^80 of those it sees.
+ * Up to 64 rows (N * Hq / Hkv) run on mma.sync, in items of at most 32 that read each
+ * code once; more run on tcgen05 (the workspace of 2048 and more then holds an fp16
+ * copy of the cached tokens that a table row has room for, where that is at most
+ * 1 GiB a sequence; beyond, each item converts the codes again).  These choices go by
+ * the table's width, as lengths are on the device: a table cut to the longest
+ * sequence takes the least workspace and the fewest launches.
  * Results do not depend on what else runs: the split of the keys over the GPU
  * is fixed by the lengths, and partial results merge in a fixed order.
  * workspace: rcx_attn_kv_block_workspace_size(q, cache) bytes, 256-byte

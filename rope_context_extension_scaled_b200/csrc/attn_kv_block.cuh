@@ -5,7 +5,7 @@
 // V).  For every row:  x_j = (q . k_code_j) * k_scale * log2(e) / (sqrt(d) t),
 // p_j = 2^(x_j - m), O = sum p_j v_code_j v_scale / sum p_j, LSE = ln 2 (m +
 // log2 sum p_j).  Memory-bound: every code and scale a row sees is read once
-// per (sequence, KV head), for all its rows together.
+// per item, that is for up to 32 rows of a (sequence, KV head) together.
 //
 // A warp takes 32-key tiles through a ring of cp.async stages and computes, per
 // 16 keys, S^T = K Q^T and O^T += V^T P^T on fp16 MMAs (m16n8k16, fp32
