@@ -263,6 +263,30 @@ def test_nan_scale_reaches_rows_that_give_it_no_weight(G, N, start):
     assert torch.isnan(o2).all() and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+@pytest.mark.parametrize("G,N", SHAPES)
+def test_one_key_takes_everything(kind, G, N):
+    """Logits of 1e30 over scales far apart and zero: the winner's value, alone."""
+    block, start = 16, 200
+    c = filled([start + N], block, 1, 64, kind, seed=3)
+    row = c.table[0].long()
+    c.v_scale[row] *= torch.exp2(10.0 * torch.randint(-4, 5, (len(row), 1), generator=gen(8), device=DEV))
+    c.v_scale[row[::3]] = 0
+    q, o, lse = attend(c, G, [start], [N], N, 64, qscale=1e30, out=torch.float32)
+    K, V = values(c, 0, start + N)
+    checked = 0
+    for h in range(G):
+        z = np64(q[0, :, h]) @ K[:, 0].T
+        for i in range(N):
+            top = z[i, :start + 1 + i]
+            best = int(top.argmax())
+            if top[best] - np.partition(top, -2)[-2] > 1e-4 * np.abs(top[best]):   # fp32 sums cannot mistake the winner
+                # three half steps of fp16 of its own value: no other key has any weight
+                assert np.abs(np64(o[0, i, h]) - V[best, 0]).max() <= 3 * 2.0 ** -11 * np.abs(V[best, 0]).max()
+                checked += 1
+    assert checked
+
+
 # ------------------------------------------------------------------ tables with room for more
 
 @pytest.mark.parametrize("kind", ["int8", "e4m3"])
